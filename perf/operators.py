@@ -3,7 +3,7 @@
 Four operators:
 
 * ``route``    moe_route_scored: softmax or sigmoid scores, a balance bias, expert groups, top-k, renormalised weights
-* ``quantize`` moe_mx_quantize and moe_mx_dequantize: rows (gathered in expert order or not) to MXFP4 and back to values
+* ``quantize`` moe_mx_quantize and moe_mx_dequantize: rows (each written to its experts' places, or as they are) to MXFP4 and back to values
 * ``product``  moe_mx_grouped_gemm: rows in MXFP4 against expert matrices in MXFP4
 * ``ffn``      moe_mx_quantize and moe_grouped_ffn_mx: an expert SwiGLU FFN from bf16 tokens to permuted outputs
 
@@ -36,9 +36,9 @@ def listed():
         # the largest batch, an odd number of tokens, wide rows
         dict(name="route prefill 8191", op="route", T=8191, d=4096, E=256, k=8, scoring="sigmoid", bias=True, groups=1,
              kept=1, group_top=1, renorm=True, scale=1.0),
-        # the rows of one decode step's 8 tokens, gathered for their experts
+        # the rows of one decode step's 8 tokens, each for its 8 experts
         dict(name="quantize decode 8", op="quantize", T=8, K=2048, k=8, dtype="bf16"),
-        # the activations of the 4096-token prefill, gathered in expert order
+        # the activations of the 4096-token prefill, in expert order
         dict(name="quantize gather 4096", op="quantize", T=4096, K=2048, k=8, dtype="bf16"),
         # fp32 rows as they are (weights, or a checkpoint's tensor), an odd number of them
         dict(name="quantize fp32 28673", op="quantize", T=28673, K=4096, k=0, dtype="fp32"),
@@ -108,7 +108,7 @@ def _matrix(w):
 
 
 def _routing(case, gen):
-    """Distinct random experts for each token, rows sorted by expert: perm, offsets, and the experts with rows."""
+    """Distinct random experts for each token, rows sorted by expert: perm, offsets, the experts with rows, the longest run."""
     T, E, k = case["T"], case["E"], case["k"]
     ids = torch.rand(T, E, generator=gen, device="cuda").argsort(-1)[:, :k].reshape(-1)
     perm = torch.argsort(ids, stable=True)
@@ -116,6 +116,12 @@ def _routing(case, gen):
     offsets = torch.zeros(E + 1, dtype=torch.int32, device="cuda")
     offsets[1:] = counts.cumsum(0)
     return perm.int(), offsets, counts.nonzero().reshape(-1), int(counts.max())
+
+
+def _inverse(perm):
+    inv = torch.empty_like(perm)
+    inv[perm.long()] = torch.arange(perm.numel(), dtype=torch.int32, device=perm.device)
+    return inv
 
 
 _DTYPES = {"bf16": torch.bfloat16, "fp16": torch.float16, "fp32": torch.float32}
@@ -137,6 +143,7 @@ def prepare(case, seed):
         # magnitudes over a few octaves from row to row, as hidden states have them
         s["x"] = (normal(T, case["K"]) * torch.exp2(normal(T, 1))).to(_DTYPES[case["dtype"]])
         s["perm"] = torch.randperm(T * case["k"], generator=g, device="cuda").int() if case["k"] else None
+        s["inv_perm"] = _inverse(s["perm"]) if case["k"] else None
     elif op == "product":
         s["perm"], s["offsets"], s["active"], s["cap"] = _routing(case, g)
         N, K = case["N"], case["K"]
@@ -145,6 +152,7 @@ def prepare(case, seed):
         s["mats"] = torch.stack([_matrix(normal(N, K, std=GATE_STD)) for _ in range(case["E"])])
     else:
         s["perm"], s["offsets"], s["active"], s["cap"] = _routing(case, g)
+        s["inv_perm"] = _inverse(s["perm"])
         d, F = case["d"], case["F"]
         s["x"] = normal(T, d).bfloat16()
         blobs = []
@@ -262,12 +270,12 @@ def _run_own(state, case, op):
             topk_groups=case["kept"], group_top=case["group_top"], renorm=case["renorm"], scale=case["scale"])
         return {"idx": idx, "w": w}
     if op == "quantize":
-        codes, scales = moeq.moe_mx_quantize(state["x"], perm=state["perm"], k=max(1, case["k"]))
+        codes, scales = moeq.moe_mx_quantize(state["x"], inv_perm=state["inv_perm"], k=max(1, case["k"]))
         return moeq.moe_mx_dequantize(codes, scales, dtype=torch.bfloat16)
     if op == "product":
         return moeq.moe_mx_grouped_gemm(state["codes"], state["scales"], state["offsets"], state["mats"], case["N"],
                                         dtype=_DTYPES[case["out"]])
-    codes, scales = moeq.moe_mx_quantize(state["x"], perm=state["perm"], k=case["k"])
+    codes, scales = moeq.moe_mx_quantize(state["x"], inv_perm=state["inv_perm"], k=case["k"])
     return moeq.moe_grouped_ffn_mx(codes, scales, state["offsets"], state["blobs"], case["F"])
 
 
