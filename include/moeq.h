@@ -184,6 +184,41 @@ MOE_API moe_status_t moe_route_topk_noalloc(const void* x, const float* w_router
                                             const int32_t* forced_idx, int T, int d, int E, int k,
                                             int32_t* topk_idx, float* topk_w, moe_stream_t stream);
 
+/* moe_route_scored -- router with scores, a balance bias and expert groups
+ * ([D2MoE] Dual Routing, expert gate, in the form of layers with many
+ * experts).  For logits l[t][e] = sum_i x[t][i] * w_router[e][i]:
+ *   s[t][e] = softmax over e of l (MOE_SCORE_SOFTMAX) or sigmoid(l)
+ *             (MOE_SCORE_SIGMOID)
+ *   c[t][e] = s[t][e] + bias[e]: what the choice compares.  bias fp32 [E] or
+ *             NULL (0); -inf takes an expert out of the choice for as long
+ *             as others are left.
+ *   groups: the E experts are n_groups runs of E / n_groups; a group's score
+ *             is its largest c (group_top = 1) or the sum of its two largest
+ *             (group_top = 2); the topk_groups best groups stay (equal
+ *             scores: the lower group)
+ *   topk_idx int32 [T][k]: the k largest c of the groups that stay, in
+ *             descending order, equal values to the lower index.  The choice
+ *             is that of c in exact arithmetic, evaluated in fp64 where the
+ *             fp32 values' error bounds leave it open (without a bias and
+ *             with group_top = 1, or without groups, the logits themselves
+ *             are compared).
+ *             A c that is NaN counts as -inf.
+ *   topk_w   fp32 [T][k]: s of the picks, divided by the sum over the picks
+ *             when renorm != 0 (0 where that sum is 0), times scale; the bias
+ *             does not enter.
+ *   workspace >= moe_route_scored_workspace_bytes(T, d, E) bytes of device
+ *             scratch, 16-byte aligned (x and w_router too).
+ * topk_idx and topk_w are what moe_permute and moe_unpermute_combine take.
+ * Requires 1 <= k <= E <= 256, k <= 16, d % 32 == 0, n_groups <= 32 dividing
+ * E, group_top experts or more to a group and k or more in the groups that
+ * stay. */
+typedef enum { MOE_SCORE_SOFTMAX = 0, MOE_SCORE_SIGMOID = 1 } moe_scoring_t;
+MOE_API moe_status_t moe_route_scored(const void* x, const float* w_router, const float* bias, int T, int d, int E,
+                                      int k, int scoring, int n_groups, int topk_groups, int group_top, int renorm,
+                                      double scale, int32_t* topk_idx, float* topk_w, void* workspace,
+                                      size_t workspace_bytes, moe_stream_t stream);
+MOE_API size_t moe_route_scored_workspace_bytes(int T, int d, int E);
+
 /* moe_permute -- per-expert histogram, exclusive prefix sum and stable
  * permutation of the T*k assignments a = t*k + j ([Read-ME] expert-aware
  * batching; [ExactMoE] grouped execution).  No atomics: per-block
@@ -331,6 +366,93 @@ MOE_API moe_status_t moe_static_bits(const int32_t* topk_idx, const uint8_t* wid
 MOE_API moe_status_t moe_unpermute_combine(const void* y_perm, const int32_t* inv_perm,
                                    const float* topk_w, const void* residual, int T, int k, int d,
                                    void* y, moe_stream_t stream);
+
+/* ---------------------------------------------------------------------
+ * MXFP4: 4-bit floating-point weights and activations (the OCP
+ * microscaling format; the same layer as above with both operands of its
+ * products in 4 bits).  Elements are e2m1 (0, 0.5, 1, 1.5, 2, 3, 4, 6 and
+ * their negatives; code bit 3 is the sign), and 32 consecutive elements
+ * along K share a scale 2^(byte - 127); byte 255 makes the block NaN.
+ *   quantise: a = max |v| of the block, S = floor(log2 a) - 2 clamped to
+ *   [-127, 127], byte = S + 127 (0 for a block of zeros), code = v / 2^S
+ *   rounded half to even, saturating at 6.  A block with an Inf or a NaN
+ *   gets byte 255 and codes 0, and flags MOE_DEV_RANGE.
+ * Codes are two to a byte, element 2i in the low nibble.
+ *   Rows (activations): codes [rows][K/2], scales [rows][K/32], K % 32 == 0.
+ *   A weight matrix [N][K] (N, K multiples of 128) is one block of
+ *   moe_mx_matrix_bytes(N, K) = N K 17/32 bytes: its codes [N][K/2], then
+ *   its scales in tiles of 128 rows x 128 K, 512 bytes each, K inside a row
+ *   of tiles; inside a tile row r, 32-block b is byte
+ *   (r % 32) * 16 + (r / 32) * 4 + b.
+ *   An expert's FFN blob (moe_mx_blob_bytes(d, F) bytes) is the matrix
+ *   [2F][d] of its gate and up rows (32 gate rows, the 32 up rows of the same
+ *   features, the next 32 gate rows, ...), then the matrix [d][F] of W_down.
+ * Both size functions return 0 for a size they do not support.
+ * ------------------------------------------------------------------ */
+typedef enum { MOE_F32 = 0, MOE_BF16 = 1, MOE_F16 = 2 } moe_dtype_t;
+MOE_API size_t moe_mx_matrix_bytes(int N, int K);
+MOE_API size_t moe_mx_blob_bytes(int d, int F);
+
+/* moe_mx_quantize -- rows to MXFP4, written in expert order or as they are.
+ *   x        [rows][K] of `dtype` (moe_dtype_t), rows `ld` elements apart
+ *   inv_perm int32 [rows][k] or NULL.  Given (from moe_permute): row t is
+ *            quantised once and written to the k rows inv_perm[t][j] of the
+ *            output, which has rows * k rows.  NULL: k = 1, row t to row t.
+ *   codes    [rows * k][K/2], scales [rows * k][K/32]
+ * Places outside [0, rows * k) are skipped and flag MOE_DEV_BAD_INDEX in
+ * `status` (may be NULL); output rows that no place names keep what they
+ * held.  Requires K % 32 == 0, rows a multiple of 16 bytes apart, x and codes
+ * 16-byte aligned, rows * k < 2^31. */
+MOE_API moe_status_t moe_mx_quantize(const void* x, int dtype, int rows, int K, size_t ld, const int32_t* inv_perm,
+                                     int k, void* codes, void* scales, int32_t* status, moe_stream_t stream);
+
+/* moe_mx_dequantize -- the values rows of MXFP4 stand for, out [rows][K] in
+ * `dtype` MOE_F32 or MOE_BF16.  Both hold every value exactly, but for those
+ * of 2^128 and more that scale bytes 253 and 254 can give (moe_mx_quantize
+ * makes none): they become Inf.  codes and out 16-byte aligned. */
+MOE_API moe_status_t moe_mx_dequantize(const void* codes, const void* scales, int rows, int K, int dtype, void* out,
+                                       moe_stream_t stream);
+
+/* moe_mx_pack -- offline: E matrices w [E][N][K] of `dtype` into E MXFP4
+ * matrices, one after another.  moe_mx_pack_ffn -- offline: w_gate, w_up
+ * [E][F][d] and w_down [E][d][F] into E FFN blobs.  All 16-byte aligned. */
+MOE_API moe_status_t moe_mx_pack(const void* w, int dtype, int E, int N, int K, void* mats, int32_t* status,
+                                 moe_stream_t stream);
+MOE_API moe_status_t moe_mx_pack_ffn(const void* w_gate, const void* w_up, const void* w_down, int dtype, int E, int d,
+                                     int F, void* blobs, int32_t* status, moe_stream_t stream);
+
+/* moe_mx_grouped_gemm -- y[p][n] = sum_i W_e[n][i] xq[p][i] for the rows p in
+ * [offsets[e], offsets[e + 1]) of each expert e ([ExactMoE] grouped
+ * execution), xq and W_e the values of the MXFP4 rows and matrices.  (A plain
+ * matrix is E = 1, offsets = {0, rows}.)
+ *   codes, scales  the rows (moe_mx_quantize); offsets int32 [E + 1] (device;
+ *                  moe_permute); mats E matrices (moe_mx_pack)
+ *   out            [rows][N] of `out_dtype` (MOE_F32, MOE_BF16 or MOE_F16)
+ * Products are exact, sums fp32, the result rounded once; rows that belong to
+ * no expert keep what they held.  An fp16 output beyond the range flags
+ * MOE_DEV_RANGE, offsets outside [0, rows] are clamped and flag
+ * MOE_DEV_BAD_INDEX.  Requires N, K multiples of 128, E <= 256 and 16-byte
+ * aligned codes, scales, mats and out. */
+MOE_API moe_status_t moe_mx_grouped_gemm(const void* codes, const void* scales, const int32_t* offsets,
+                                         const void* mats, int rows, int E, int N, int K, int out_dtype, void* out,
+                                         int32_t* status, moe_stream_t stream);
+
+/* moe_grouped_ffn_mx -- the grouped expert FFN on MXFP4 rows and blobs, the
+ * MXFP4 counterpart of moe_grouped_ffn_wq:
+ *     h[p]      = silu(Wg_e xq[p]) * (Wu_e xq[p])      in fp32
+ *     y_perm[p] = Wd_e hq[p],  hq[p] = MXFP4 of h[p]
+ *   codes, scales  rows of d (moe_mx_quantize); offsets int32 [E + 1]; blobs
+ *                  E FFN blobs (moe_mx_pack_ffn)
+ *   workspace      >= moe_ffn_mx_workspace_bytes(rows, F) bytes (hq), 16-byte
+ *                  aligned
+ *   y_perm         fp16 [rows][d], for moe_unpermute_combine
+ * Sums are fp32, y_perm rounded once; range, offsets and requirements as in
+ * moe_mx_grouped_gemm (a block of h with an Inf or a NaN flags MOE_DEV_RANGE
+ * too), d and F multiples of 128. */
+MOE_API moe_status_t moe_grouped_ffn_mx(const void* codes, const void* scales, const int32_t* offsets,
+                                        const void* blobs, int rows, int E, int d, int F, void* workspace,
+                                        size_t workspace_bytes, void* y_perm, int32_t* status, moe_stream_t stream);
+MOE_API size_t moe_ffn_mx_workspace_bytes(int rows, int F);
 
 /* ---------------------------------------------------------------------
  * Offload mode ([ExactMoE] compressed experts in host memory, GPU slot

@@ -1,0 +1,653 @@
+// Grouped product of MXFP4 rows and MXFP4 expert matrices on the block-scaled
+// tensor-core instruction, y[p] = W_e xq[p] for the rows p of each expert e,
+// and the expert SwiGLU FFN built from two of them.
+//
+// An instruction multiplies e2m1 codes and applies both operands' scales
+// (one per 32 K) itself, accumulating in fp32 in tensor memory: nothing is
+// dequantised, so the kernel only has to move bytes.  The rows of an expert
+// are the M side (128 to a tile) and its weight rows the N side, so that a
+// thread of the epilogue holds consecutive outputs of one row: a block of 32
+// hidden values and its scale are formed in one thread's registers when the
+// SwiGLU output is quantised again for the second product.  (With few rows
+// the M side is mostly empty; the tensor cores then do up to 128 times the
+// work asked for, but at 17/32 byte per weight the weight stream, not the
+// tensor pipe, is the bound: a stage of 256 weight rows x 256 K takes four
+// instructions of about 128 cycles and 34 KB, which at the memory's share
+// per SM of about 23 bytes a cycle arrive in 1500.)
+//
+// Warps: 0 loads codes (TMA, 128B swizzle; the rows in boxes of 32, so that
+// a short tile does not read past its share) and weight scales (bulk copies
+// of scale tiles); 3 loads the rows' scales, which lie row by row (row
+// offsets of a bin are arbitrary, so they cannot come as tiles), and writes
+// them in tile order; 1 issues the scale copies into tensor memory and the
+// products; 4-7 are the epilogue; 2 allocates tensor memory.  Scale columns
+// belong to a pipeline stage, so a copy never meets a product that still
+// reads them.  Every wait is bounded; on a timeout the CTA raises
+// MOE_DEV_TIMEOUT, lets its copies land, frees tensor memory and returns.
+#include <cudaTypedefs.h>
+
+#include <atomic>
+#include <mutex>
+
+#include "mx.cuh"
+#include "ptx.cuh"
+
+namespace moeq {
+namespace {
+
+using namespace ptx;
+
+constexpr int kThreads = 256;
+constexpr int kM = 128;       // rows of a tile
+constexpr int kKS = 256;      // K of a stage (128 bytes of codes)
+constexpr int kABox = 32;     // rows of one activation box
+
+template <int NT>
+struct Cfg {
+  static constexpr int RT = NT > 128 ? 2 : 1;  // 128-row scale tiles of the weight tile
+  static constexpr int STAGES = NT == 256 ? 4 : NT == 128 ? 6 : 7;
+  static constexpr int ACC = NT == 256 ? 1 : 2;  // accumulator buffers
+  static constexpr int A_BYTES = kM * 128;
+  static constexpr int B_BYTES = NT * 128;
+  static constexpr int SA_BYTES = 1024;       // two 128-K scale tiles
+  static constexpr int SB_BYTES = RT * 1024;
+  static constexpr int OFF_B = STAGES * A_BYTES;
+  static constexpr int OFF_SA = OFF_B + STAGES * B_BYTES;
+  static constexpr int OFF_SB = OFF_SA + STAGES * SA_BYTES;
+  static constexpr int OFF_OUT = OFF_SB + STAGES * SB_BYTES;  // 4 warps x 32 rows x 128 bytes
+  static constexpr int OFF_TILE = OFF_OUT + 4 * 4096;         // int tile_start[E + 1], off[E + 1]
+  static constexpr int OFF_BAR = OFF_TILE + 2 * (kMxMaxExperts + 1) * 4;
+  static constexpr int N_BARS = 2 * STAGES + 2 * ACC + 2;
+  static constexpr int OFF_MISC = OFF_BAR + N_BARS * 8;
+  static constexpr int SMEM = OFF_MISC + 16 + 1024;
+  static constexpr int SF_COLS = 8 + 8 * RT;  // scale columns of a stage
+  static constexpr int SF0 = ACC * NT;
+  static constexpr int TMEM_COLS = SF0 + STAGES * SF_COLS <= 256 ? 256 : 512;
+  static_assert(SF0 + STAGES * SF_COLS <= 512, "tensor memory");
+  static_assert(SMEM <= 232448, "shared memory");
+};
+
+struct Params {
+  CUtensorMap a;  // codes of the rows: bytes [rows][K/2]
+  CUtensorMap b;  // codes of the matrices: bytes [E][N][K/2]
+  const uint8_t* a_scales;
+  const uint8_t* b_scales;  // scale section of matrix 0
+  size_t mat_stride;
+  const int32_t* offsets;
+  int rows, E, N, K;
+  void* out;
+  uint8_t* out_scales;
+  int32_t* status;
+};
+
+struct Tile {
+  int e, row0, nrows, n0, nn;
+};
+
+template <int NT>
+__device__ __forceinline__ Tile decode_tile(int t, const int* tile_start, const int* off, int E, int N) {
+  int lo = 0, hi = E;  // largest e with tile_start[e] <= t
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (tile_start[mid] <= t) lo = mid; else hi = mid;
+  }
+  Tile T;
+  T.e = lo;
+  const int n = off[lo + 1] - off[lo];
+  const int mt = (n + kM - 1) / kM;
+  const int local = t - tile_start[lo];
+  // row tiles inside a weight tile: CTAs that run together share its codes
+  const int nb = local / mt, mb = local - nb * mt;
+  T.row0 = off[lo] + mb * kM;
+  T.nrows = min(kM, n - mb * kM);
+  T.n0 = nb * NT;
+  T.nn = min(NT, N - T.n0);
+  return T;
+}
+
+template <int NT, int OUT>
+__global__ void __launch_bounds__(kThreads, 1) k_mx_gemm(const __grid_constant__ Params P) {
+  using C = Cfg<NT>;
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  int* tile_start = reinterpret_cast<int*>(smem + C::OFF_TILE);
+  int* off_s = tile_start + (kMxMaxExperts + 1);
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::OFF_MISC);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::OFF_MISC + 4);
+  const uint32_t bar0 = smem_u32(smem + C::OFF_BAR);
+  auto full = [&](int i) { return bar0 + 8u * i; };
+  auto empty = [&](int i) { return bar0 + 8u * (C::STAGES + i); };
+  auto acc_full = [&](int i) { return bar0 + 8u * (2 * C::STAGES + i); };
+  auto acc_empty = [&](int i) { return bar0 + 8u * (2 * C::STAGES + C::ACC + i); };
+  const uint32_t drain_bar = bar0 + 8u * (2 * C::STAGES + 2 * C::ACC);
+  const uint32_t exit_bar = drain_bar + 8u;
+
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int E = P.E, NB = (P.N + NT - 1) / NT;
+  const int KB = (P.K + kKS - 1) / kKS;  // stages of a tile; the last may hold 128 K
+
+  if (tid == 0) {
+    for (int i = 0; i < C::STAGES; ++i) {
+      mbar_init(full(i), 2);  // the codes producer, the row-scale warp
+      mbar_init(empty(i), 1);
+    }
+    for (int i = 0; i < C::ACC; ++i) {
+      mbar_init(acc_full(i), 1);
+      mbar_init(acc_empty(i), 4);
+    }
+    mbar_init(drain_bar, 1);
+    mbar_init(exit_bar, kThreads / 32);
+    *abort_flag = 0;
+    mbar_init_fence();
+  }
+  if (warp == 2) tmem_alloc(smem_u32(tmem_slot), C::TMEM_COLS);
+  pdl_wait();
+  pdl_trigger();
+  // offsets are clamped into [0, rows]: no table can send a tile outside
+  for (int b = tid; b <= E; b += kThreads) {
+    const int v = P.offsets[b];
+    const int c = min(max(v, 0), P.rows);
+    if (c != v || (b == E && v != P.rows)) flag_status(P.status, MOE_DEV_BAD_INDEX);
+    off_s[b] = c;
+  }
+  __syncwarp();
+  __syncthreads();
+  if (warp == 0) {  // tiles per expert -> exclusive scan, a run of experts per lane
+    const int per = (E + 31) / 32, b0 = lane * per;
+    int run = 0;
+    for (int i = 0; i < per; ++i) {
+      const int b = b0 + i;
+      if (b < E) {
+        const int n = max(0, off_s[b + 1] - off_s[b]);
+        tile_start[b] = run;
+        run += (n + kM - 1) / kM * NB;
+      }
+    }
+    int incl = run;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int v = __shfl_up_sync(0xffffffffu, incl, o);
+      if (lane >= o) incl += v;
+    }
+    for (int i = 0; i < per; ++i)
+      if (b0 + i < E) tile_start[b0 + i] += incl - run;
+    if (lane == 31) tile_start[E] = incl;
+  }
+  __syncwarp();
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  const int tiles = tile_start[E];
+
+  if (warp == 0) {
+    // ---- codes and weight scales ------------------------------------------
+    if (lane == 0) {
+      int s = 0, ph = 0;
+      bool ok = true;
+      for (int t = blockIdx.x; t < tiles && ok; t += gridDim.x) {
+        const Tile T = decode_tile<NT>(t, tile_start, off_s, E, P.N);
+        const int boxes = (T.nrows + kABox - 1) / kABox;
+        const int rts = C::RT == 2 && T.nn > 128 ? 2 : 1;
+        const uint8_t* sc = P.b_scales + static_cast<size_t>(T.e) * P.mat_stride;
+        for (int kb = 0; kb < KB; ++kb) {
+          ok = mbar_wait(empty(s), ph ^ 1, abort_flag, P.status);
+          if (!ok) break;
+          const uint32_t halves = P.K - kb * kKS > 128 ? 2 : 1;
+          mbar_expect_tx(full(s), boxes * (kABox * 128) + C::B_BYTES + rts * halves * 512);
+          const uint32_t adst = smem_u32(smem + s * C::A_BYTES);
+          for (int i = 0; i < boxes; ++i)
+            tma_load_2d(adst + i * (kABox * 128), &P.a, kb * 128, T.row0 + i * kABox, full(s));
+          tma_load_3d(smem_u32(smem + C::OFF_B + s * C::B_BYTES), &P.b, kb * 128, T.n0, T.e, full(s));
+          for (int r = 0; r < rts; ++r)
+            bulk_load(smem_u32(smem + C::OFF_SB + s * C::SB_BYTES + r * 1024),
+                      sc + (static_cast<size_t>((T.n0 >> 7) + r) * (P.K / 128) + 2 * kb) * 512, halves * 512, full(s));
+          if (++s == C::STAGES) { s = 0; ph ^= 1; }
+        }
+      }
+      if (!ok) {  // the copies in flight land before the CTA goes
+        const uint64_t t0 = global_ns();
+        for (int i = 0; i < C::STAGES; ++i) {
+          const int p = i < s ? ph : ph ^ 1;
+          while (!mbar_try(full(i), p, 1000u) && global_ns() - t0 < kWaitLimitNs) {}
+        }
+      }
+    }
+  } else if (warp == 3) {
+    // ---- row scales: four rows a lane, two 128-K words a stage --------------
+    constexpr int G = 4;  // stages loaded ahead of the ones being written
+    int s = 0, ph = 0;
+    bool ok = true;
+    for (int t = blockIdx.x; t < tiles && ok; t += gridDim.x) {
+      const Tile T = decode_tile<NT>(t, tile_start, off_s, E, P.N);
+      const uint8_t* base = P.a_scales + static_cast<size_t>(T.row0 + lane) * (P.K / 32);
+      auto fetch = [&](int kb0, uint4 (&w)[G][2]) {
+#pragma unroll
+        for (int g = 0; g < G; ++g) {
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const int k = (kb0 + g) * kKS + h * 128;
+            uint32_t v[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+              v[j] = k < P.K && lane + 32 * j < T.nrows
+                         ? *reinterpret_cast<const uint32_t*>(base + static_cast<size_t>(32 * j) * (P.K / 32) + k / 32)
+                         : 0u;
+            w[g][h] = make_uint4(v[0], v[1], v[2], v[3]);
+          }
+        }
+      };
+      uint4 cur[G][2], nxt[G][2];
+      fetch(0, cur);
+      for (int kb0 = 0; kb0 < KB && ok; kb0 += G) {
+        if (kb0 + G < KB) fetch(kb0 + G, nxt);
+#pragma unroll
+        for (int g = 0; g < G; ++g) {
+          if (kb0 + g < KB && ok) {
+            ok = warp_wait(empty(s), ph ^ 1, abort_flag, P.status);
+            if (ok) {
+              uint8_t* dst = smem + C::OFF_SA + s * C::SA_BYTES + lane * 16;
+              *reinterpret_cast<uint4*>(dst) = cur[g][0];
+              *reinterpret_cast<uint4*>(dst + 512) = cur[g][1];
+              fence_async_shared();
+              __syncwarp();
+              if (lane == 0) mbar_arrive(full(s));
+              if (++s == C::STAGES) { s = 0; ph ^= 1; }
+            }
+          }
+        }
+#pragma unroll
+        for (int g = 0; g < G; ++g) {
+          cur[g][0] = nxt[g][0];
+          cur[g][1] = nxt[g][1];
+        }
+      }
+    }
+  } else if (warp == 1) {
+    // ---- products -----------------------------------------------------------
+    int s = 0, ph = 0, acc = 0, aph = 0;
+    bool ok = true;
+    const uint64_t da0 = desc_sw128(smem_u32(smem)), db0 = desc_sw128(smem_u32(smem + C::OFF_B));
+    const uint64_t dsa0 = desc_plain(smem_u32(smem + C::OFF_SA)), dsb0 = desc_plain(smem_u32(smem + C::OFF_SB));
+    for (int t = blockIdx.x; t < tiles && ok; t += gridDim.x) {
+      const Tile T = decode_tile<NT>(t, tile_start, off_s, E, P.N);
+      const uint32_t id0 = idesc_mxf4(T.nn, 0), id1 = idesc_mxf4(T.nn, 1);
+      const int rts = C::RT == 2 && T.nn > 128 ? 2 : 1;
+      const uint32_t shift = NT == 64 ? (T.n0 >> 5) & 2 : 0;  // second half of a 128-row scale tile
+      ok = warp_wait(acc_empty(acc), aph ^ 1, abort_flag, P.status);
+      if (!ok) break;
+      tc_fence_after();
+      const uint32_t d = tmem + acc * NT;
+      for (int kb = 0; kb < KB; ++kb) {
+        ok = warp_wait(full(s), ph, abort_flag, P.status);
+        if (!ok) break;
+        tc_fence_after();
+        if (lane == 0) {
+          const int halves = P.K - kb * kKS > 128 ? 2 : 1;
+          const uint32_t sfa = tmem + C::SF0 + s * C::SF_COLS, sfb = sfa + 8;
+          const uint64_t da = da0 + s * (C::A_BYTES >> 4), db = db0 + s * (C::B_BYTES >> 4);
+          const uint64_t dsa = dsa0 + s * (C::SA_BYTES >> 4), dsb = dsb0 + s * (C::SB_BYTES >> 4);
+          for (int h = 0; h < halves; ++h) {
+            tc_copy_scales(sfa + 4 * h, dsa + 32 * h);
+            for (int r = 0; r < rts; ++r) tc_copy_scales(sfb + 4 * C::RT * h + 4 * r, dsb + 64 * r + 32 * h);
+          }
+          for (int h = 0; h < halves; ++h) {
+            const uint32_t fa = sfa + 4 * h, fb = sfb + 4 * C::RT * h + shift;
+            mma_mxf4(d, da + 4 * h, db + 4 * h, id0, fa, fb, (kb | h) != 0);
+            mma_mxf4(d, da + 4 * h + 2, db + 4 * h + 2, id1, fa, fb, 1u);
+          }
+          tc_commit(empty(s));
+        }
+        __syncwarp();
+        if (++s == C::STAGES) { s = 0; ph ^= 1; }
+      }
+      if (!ok) break;
+      if (lane == 0) tc_commit(acc_full(acc));
+      __syncwarp();
+      if (++acc == C::ACC) { acc = 0; aph ^= 1; }
+    }
+    // every product issued here completes before tensor memory is released
+    if (lane == 0) tc_commit(drain_bar);
+    const uint64_t t0 = global_ns();
+    while (!mbar_try(drain_bar, 0, 1000u) && global_ns() - t0 < kWaitLimitNs) {}
+    __syncwarp();
+  } else if (warp >= 4) {
+    // ---- epilogue: lane = row of the tile, quadrant = warp % 4 ----------------
+    const int q = warp & 3;
+    int acc = 0, aph = 0;
+    bool ok = true;
+    for (int t = blockIdx.x; t < tiles && ok; t += gridDim.x) {
+      const Tile T = decode_tile<NT>(t, tile_start, off_s, E, P.N);
+      ok = warp_wait(acc_full(acc), aph, abort_flag, P.status);
+      if (!ok) break;
+      tc_fence_after();
+      const uint32_t tb = tmem + (static_cast<uint32_t>(32 * q) << 16) + acc * NT;
+      const int r = 32 * q + lane;
+      const bool live = r < T.nrows;
+      const bool any = 32 * q < T.nrows;
+      bool bad = false;
+      if (OUT == kMxOutSwiglu) {
+        // columns: 32 gate rows, 32 up rows, ...; each pair is one 32-block of h
+        uint8_t* hc = static_cast<uint8_t*>(P.out) + static_cast<size_t>(T.row0 + r) * (P.N / 4) + T.n0 / 4;
+        uint8_t* hs = P.out_scales + static_cast<size_t>(T.row0 + r) * (P.N / 64) + T.n0 / 64;
+        if (any) {
+          for (int c = 0; c < T.nn; c += 64) {
+            uint32_t g[32], u[32];
+            tmem_ld32(tb + c, g);
+            tmem_ld32(tb + c + 32, u);
+            tmem_ld_wait();
+            float h[32];
+            uint32_t m = 0;
+#pragma unroll
+            for (int i = 0; i < 32; ++i) {
+              h[i] = silu_f(__uint_as_float(g[i])) * __uint_as_float(u[i]);
+              m = max(m, __float_as_uint(h[i]) & 0x7FFFFFFFu);
+            }
+            const uint32_t byte = mx_scale_byte(m);
+            uint32_t w[4] = {0, 0, 0, 0};
+            if (byte != 255u) {
+              const float inv = mx_inv_scale(byte);
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                float v[8];
+#pragma unroll
+                for (int j = 0; j < 8; ++j) v[j] = h[8 * i + j] * inv;
+                w[i] = mx_encode8(v);
+              }
+            }
+            if (live) {
+              bad |= byte == 255u;
+              *reinterpret_cast<uint4*>(hc + c / 4) = make_uint4(w[0], w[1], w[2], w[3]);
+              hs[c / 64] = static_cast<uint8_t>(byte);
+            }
+          }
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(acc_empty(acc));
+      } else {
+        // 128 bytes of every row at a time through the warp's staging rows
+        // (16-byte pieces XOR-swizzled by row), so that a store instruction
+        // covers four whole 128-byte runs
+        constexpr int ES = OUT == kMxOutF32 ? 4 : 2, CW = 128 / ES;
+        uint8_t* st = smem + C::OFF_OUT + q * 4096;
+        uint8_t* out = static_cast<uint8_t*>(P.out);
+        if (any) {
+          for (int c = 0; c < T.nn; c += CW) {
+            uint32_t v[CW / 32][32];
+#pragma unroll
+            for (int i = 0; i < CW / 32; ++i) tmem_ld32(tb + c + 32 * i, v[i]);
+            tmem_ld_wait();
+            __syncwarp();  // the rows staged before have been read
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+              uint32_t w[4];
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                if (OUT == kMxOutF32) {
+                  w[i] = v[0][4 * j + i];
+                } else {
+                  const int at = 8 * j + 2 * i;
+                  const float y0 = __uint_as_float(v[at / 32][at % 32]), y1 = __uint_as_float(v[at / 32][at % 32 + 1]);
+                  if (OUT == kMxOutF16) {
+                    bad |= !(fmaxf(fabsf(y0), fabsf(y1)) <= 65504.0f) || y0 != y0 || y1 != y1;
+                    const __half2 h = __floats2half2_rn(y0, y1);
+                    w[i] = *reinterpret_cast<const uint32_t*>(&h);
+                  } else {
+                    const __nv_bfloat162 h = __floats2bfloat162_rn(y0, y1);
+                    w[i] = *reinterpret_cast<const uint32_t*>(&h);
+                  }
+                }
+              }
+              *reinterpret_cast<uint4*>(st + lane * 128 + ((j ^ (lane & 7)) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
+            }
+            __syncwarp();
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              const int row = 4 * i + (lane >> 3), j = lane & 7;
+              if (32 * q + row < T.nrows)
+                *reinterpret_cast<uint4*>(out + (static_cast<size_t>(T.row0 + 32 * q + row) * P.N + T.n0 + c) * ES +
+                                          j * 16) =
+                    *reinterpret_cast<const uint4*>(st + row * 128 + ((j ^ (row & 7)) << 4));
+            }
+          }
+        }
+        bad = bad && live;
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(acc_empty(acc));
+      }
+      if (bad) flag_status(P.status, MOE_DEV_RANGE);
+      if (++acc == C::ACC) { acc = 0; aph ^= 1; }
+    }
+  }
+
+  __syncwarp();
+  tc_fence_before();
+  if (lane == 0) mbar_arrive(exit_bar);
+  if (warp == 2) {  // frees tensor memory once every warp has left its loop
+    const uint64_t t0 = global_ns();
+    while (!mbar_try(exit_bar, 0, 1000u) && global_ns() - t0 < 2 * kWaitLimitNs) {}
+    __syncwarp();
+    tc_fence_after();
+    tmem_free(tmem, C::TMEM_COLS);
+  }
+}
+
+// ---- host side ----------------------------------------------------------------
+
+PFN_cuTensorMapEncodeTiled_v12000 get_encode() {
+  static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
+  static std::once_flag once;
+  std::call_once(once, [] {
+    void* p = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &p, cudaEnableDefault, &q) == cudaSuccess &&
+        q == cudaDriverEntryPointSuccess)
+      fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(p);
+  });
+  return fn;
+}
+
+bool encode_bytes(CUtensorMap* m, int rank, const void* base, const cuuint64_t* dims, const cuuint64_t* strides,
+                  const cuuint32_t* box) {
+  auto fn = get_encode();
+  if (!fn) return false;
+  const cuuint32_t es[3] = {1, 1, 1};
+  return fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, rank, const_cast<void*>(base), dims, strides, box, es,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <int NT, int OUT>
+moe_status_t launch(const MxGemmArgs& a, cudaStream_t s) {
+  Params P{};
+  {
+    const cuuint64_t dims[2] = {static_cast<cuuint64_t>(a.K / 2), static_cast<cuuint64_t>(a.rows)};
+    const cuuint64_t str[1] = {static_cast<cuuint64_t>(a.K / 2)};
+    const cuuint32_t box[2] = {128, kABox};
+    const cuuint64_t dimb[3] = {static_cast<cuuint64_t>(a.K / 2), static_cast<cuuint64_t>(a.N),
+                                static_cast<cuuint64_t>(a.E)};
+    const cuuint64_t strb[2] = {static_cast<cuuint64_t>(a.K / 2), static_cast<cuuint64_t>(a.mat_stride)};
+    const cuuint32_t boxb[3] = {128, NT, 1};
+    if (!encode_bytes(&P.a, 2, a.a_codes, dims, str, box) || !encode_bytes(&P.b, 3, a.mats, dimb, strb, boxb)) {
+      set_error("tensor map (MXFP4 codes) could not be encoded");
+      return MOE_ERR_CUDA;
+    }
+  }
+  P.a_scales = a.a_scales;
+  P.b_scales = a.mats + static_cast<size_t>(a.N) * (a.K / 2);
+  P.mat_stride = a.mat_stride;
+  P.offsets = a.offsets;
+  P.rows = a.rows;
+  P.E = a.E;
+  P.N = a.N;
+  P.K = a.K;
+  P.out = a.out;
+  P.out_scales = a.out_scales;
+  P.status = a.status;
+  // shared-memory opt-in: a per-device attribute, set once per device (the
+  // first call on a device precedes any stream capture)
+  static std::atomic<uint64_t> attr_set{0};
+  static std::atomic<int> sms[64] = {};
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return cuda_check(e, "MXFP4 product: cudaGetDevice");
+  if (dev < 0 || dev >= 64) {
+    set_error("MXFP4 product: device %d beyond the supported 64", dev);
+    return MOE_ERR_UNSUPPORTED_SHAPE;
+  }
+  auto kern = k_mx_gemm<NT, OUT>;
+  if (!(attr_set.load() & (1ull << dev))) {
+    int n = 0;
+    e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg<NT>::SMEM);
+    if (e == cudaSuccess) e = cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev);
+    if (e != cudaSuccess) return cuda_check(e, "MXFP4 product: shared-memory attribute");
+    sms[dev].store(n);
+    attr_set.fetch_or(1ull << dev);
+  }
+  const long most = (static_cast<long>(a.rows) / kM + std::min(a.E, a.rows)) * ceil_div(a.N, NT);
+  const int grid = static_cast<int>(std::min<long>(most, sms[dev].load()));
+  return cuda_check(launch_pdl(pdl_for(a.rows), kern, dim3(grid), dim3(kThreads), Cfg<NT>::SMEM, s, P),
+                    "MXFP4 product launch");
+}
+
+template <int OUT>
+moe_status_t launch_out(const MxGemmArgs& a, cudaStream_t s) {
+  // Widest weight tile that still gives every SM one: wide tiles read the
+  // rows fewer times, narrow ones spread a small call's weights over more SMs.
+  const long mt = std::max<long>(std::min(a.E, a.rows), a.rows / kM);
+  if (mt * (a.N / 256) >= 148) return launch<256, OUT>(a, s);
+  if (mt * (a.N / 128) >= 148) return launch<128, OUT>(a, s);
+  return launch<64, OUT>(a, s);
+}
+
+}  // namespace
+
+moe_status_t launch_mx_gemm(const MxGemmArgs& a, cudaStream_t s) {
+  if (a.rows == 0) return MOE_OK;
+  switch (a.out_kind) {
+    case kMxOutF16: return launch_out<kMxOutF16>(a, s);
+    case kMxOutBf16: return launch_out<kMxOutBf16>(a, s);
+    case kMxOutF32: return launch_out<kMxOutF32>(a, s);
+    default: return launch_out<kMxOutSwiglu>(a, s);
+  }
+}
+
+namespace {
+
+bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+
+// Checks shared by the two entry points.
+moe_status_t check(const char* fn, const void* codes, const void* scales, const int32_t* offsets, const void* mats,
+                   const void* out, int rows, int E, int N, int K) {
+  if (rows < 0 || E <= 0 || N <= 0 || K <= 0) {
+    set_error("%s: bad sizes rows=%d E=%d N=%d K=%d", fn, rows, E, N, K);
+    return MOE_ERR_INVALID_ARG;
+  }
+  if (N % 128 || K % 128 || N > (1 << 24) || K > (1 << 24) || E > kMxMaxExperts) {
+    set_error("%s: N=%d and K=%d must be multiples of 128 (up to 2^24), E=%d at most %d", fn, N, K, E, kMxMaxExperts);
+    return MOE_ERR_UNSUPPORTED_SHAPE;
+  }
+  // tile numbers and row tiles are 32-bit
+  if ((static_cast<long>(rows) / kM + E) * (N / 64) > 0x7FFFFFFFL) {
+    set_error("%s: rows=%d x N=%d is more than 2^31 - 1 tiles", fn, rows, N);
+    return MOE_ERR_UNSUPPORTED_SHAPE;
+  }
+  if (rows == 0) return MOE_OK;
+  if (!codes || !scales || !offsets || !mats || !out) {
+    set_error("%s: null pointer", fn);
+    return MOE_ERR_INVALID_ARG;
+  }
+  if (!aligned16(codes) || !aligned16(scales) || !aligned16(mats) || !aligned16(out)) {
+    set_error("%s: codes, scales, weights and output must be 16-byte aligned", fn);
+    return MOE_ERR_INVALID_ARG;
+  }
+  return MOE_OK;
+}
+
+size_t up256(size_t n) { return (n + 255) / 256 * 256; }
+
+}  // namespace
+}  // namespace moeq
+
+using namespace moeq;
+
+extern "C" {
+
+moe_status_t moe_mx_grouped_gemm(const void* codes, const void* scales, const int32_t* offsets, const void* mats,
+                                 int rows, int E, int N, int K, int out_dtype, void* out, int32_t* status,
+                                 moe_stream_t stream) {
+  const moe_status_t st = check("moe_mx_grouped_gemm", codes, scales, offsets, mats, out, rows, E, N, K);
+  if (st != MOE_OK) return st;
+  if (out_dtype != MOE_F32 && out_dtype != MOE_BF16 && out_dtype != MOE_F16) {
+    set_error("moe_mx_grouped_gemm: unknown output dtype %d", out_dtype);
+    return MOE_ERR_INVALID_ARG;
+  }
+  MxGemmArgs a{};
+  a.a_codes = static_cast<const uint8_t*>(codes);
+  a.a_scales = static_cast<const uint8_t*>(scales);
+  a.offsets = offsets;
+  a.mats = static_cast<const uint8_t*>(mats);
+  a.mat_stride = mx_matrix_bytes(N, K);
+  a.rows = rows;
+  a.E = E;
+  a.N = N;
+  a.K = K;
+  a.out_kind = out_dtype == MOE_F32 ? kMxOutF32 : out_dtype == MOE_BF16 ? kMxOutBf16 : kMxOutF16;
+  a.out = out;
+  a.status = status;
+  return launch_mx_gemm(a, static_cast<cudaStream_t>(stream));
+}
+
+size_t moe_ffn_mx_workspace_bytes(int rows, int F) {
+  if (rows <= 0 || F <= 0) return 256;
+  return up256(static_cast<size_t>(rows) * (F / 2)) + up256(static_cast<size_t>(rows) * (F / 32));
+}
+
+moe_status_t moe_grouped_ffn_mx(const void* codes, const void* scales, const int32_t* offsets, const void* blobs,
+                                int rows, int E, int d, int F, void* workspace, size_t workspace_bytes, void* y_perm,
+                                int32_t* status, moe_stream_t stream) {
+  const char* fn = "moe_grouped_ffn_mx";
+  moe_status_t st = check(fn, codes, scales, offsets, blobs, y_perm, rows, E, d, F);
+  if (st == MOE_OK) st = check(fn, codes, scales, offsets, blobs, y_perm, rows, E, 2 * F, d);
+  if (st != MOE_OK) return st;
+  if (rows == 0) return MOE_OK;
+  if (!workspace || workspace_bytes < moe_ffn_mx_workspace_bytes(rows, F)) {
+    set_error("%s: workspace %zu < %zu bytes", fn, workspace_bytes, moe_ffn_mx_workspace_bytes(rows, F));
+    return MOE_ERR_WORKSPACE;
+  }
+  if (!aligned16(workspace)) {
+    set_error("%s: workspace must be 16-byte aligned", fn);
+    return MOE_ERR_INVALID_ARG;
+  }
+  uint8_t* hc = static_cast<uint8_t*>(workspace);
+  uint8_t* hs = hc + up256(static_cast<size_t>(rows) * (F / 2));
+  MxGemmArgs a{};
+  a.a_codes = static_cast<const uint8_t*>(codes);
+  a.a_scales = static_cast<const uint8_t*>(scales);
+  a.offsets = offsets;
+  a.mats = static_cast<const uint8_t*>(blobs);
+  a.mat_stride = mx_matrix_bytes(2 * F, d) + mx_matrix_bytes(d, F);
+  a.rows = rows;
+  a.E = E;
+  a.N = 2 * F;
+  a.K = d;
+  a.out_kind = kMxOutSwiglu;
+  a.out = hc;
+  a.out_scales = hs;
+  a.status = status;
+  st = launch_mx_gemm(a, static_cast<cudaStream_t>(stream));
+  if (st != MOE_OK) return st;
+  a.a_codes = hc;
+  a.a_scales = hs;
+  a.mats = static_cast<const uint8_t*>(blobs) + mx_matrix_bytes(2 * F, d);
+  a.N = d;
+  a.K = F;
+  a.out_kind = kMxOutF16;
+  a.out = y_perm;
+  a.out_scales = nullptr;
+  return launch_mx_gemm(a, static_cast<cudaStream_t>(stream));
+}
+
+}  // extern "C"

@@ -88,3 +88,67 @@ class QuantMoELayer:
                                      residual=residual, y=v["y"], y_perm=v["y_perm"], workspace=v["workspace"],
                                      status=v["status"], stream=stream)
         return v["y"]
+
+
+class MxMoELayer:
+    """One MoE layer in MXFP4 (4-bit floating-point weights and activations)
+    behind the scored router, call by call: moe_route_scored -> moe_permute ->
+    moe_mx_quantize (each token's row once, to its experts' places) ->
+    moe_grouped_ffn_mx -> moe_unpermute_combine.  It owns the device buffers;
+    ``forward`` allocates nothing and can be captured into a graph (after one
+    call on the device)."""
+
+    def __init__(self, d, E, k, F, w_router, blobs, max_tokens, bias=None, scoring="softmax", n_groups=1,
+                 topk_groups=1, group_top=1, renorm=True, scale=1.0, device="cuda"):
+        self.d, self.E, self.k, self.F = d, E, k, F
+        self.w_router, self.bias, self.blobs = w_router, bias, blobs
+        self.routing = dict(scoring=scoring, n_groups=n_groups, topk_groups=topk_groups, group_top=group_top,
+                            renorm=renorm, scale=scale)
+        self.device = torch.device(device)
+        self.max_tokens = max_tokens
+        T, rows, dev = max_tokens, max_tokens * k, self.device
+        self.buf = dict(
+            topk_idx=torch.empty(T, k, dtype=torch.int32, device=dev),
+            topk_w=torch.empty(T, k, dtype=torch.float32, device=dev),
+            counts=torch.empty(E, dtype=torch.int32, device=dev),
+            offsets=torch.empty(E + 1, dtype=torch.int32, device=dev),
+            perm=torch.empty(rows, dtype=torch.int32, device=dev),
+            inv_perm=torch.empty(rows, dtype=torch.int32, device=dev),
+            codes=torch.empty(rows, d // 2, dtype=torch.uint8, device=dev),
+            scales=torch.empty(rows, d // 32, dtype=torch.uint8, device=dev),
+            y_perm=torch.empty(rows, d, dtype=torch.float16, device=dev),
+            y=torch.empty(T, d, dtype=torch.bfloat16, device=dev),
+            status=torch.zeros(1, dtype=torch.int32, device=dev),
+            route_ws=torch.empty(moeq.moe_route_scored_workspace_bytes(T, d, E), dtype=torch.uint8, device=dev),
+            perm_ws=torch.empty(moeq.moe_permute_workspace_bytes(T, E, k, False), dtype=torch.uint8, device=dev),
+            workspace=torch.empty(moeq.moe_ffn_mx_workspace_bytes(rows, F), dtype=torch.uint8, device=dev),
+        )
+
+    @classmethod
+    def from_weights(cls, w_router, w_gate, w_up, w_down, k, max_tokens, **routing):
+        """w_router fp32 [E][d]; w_gate, w_up [E][F][d] and w_down [E][d][F] in fp32, bf16 or fp16."""
+        E, F, d = w_gate.shape
+        return cls(d, E, k, F, w_router, moeq.moe_mx_pack_ffn(w_gate, w_up, w_down), max_tokens, device=w_gate.device,
+                   **routing)
+
+    def views(self, T):
+        rows, b = T * self.k, self.buf
+        per_token, per_row = ("topk_idx", "topk_w", "y"), ("perm", "inv_perm", "codes", "scales", "y_perm")
+        return {n: t[:T] if n in per_token else t[:rows] if n in per_row else t for n, t in b.items()}
+
+    def forward(self, x, residual=None, stream=None):
+        """One layer pass over x (bf16 [T][d]); returns a view of the layer's y buffer (bf16 [T][d])."""
+        T = x.shape[0]
+        if T > self.max_tokens:
+            raise ValueError(f"T={T} exceeds max_tokens={self.max_tokens}")
+        v = self.views(T)
+        moeq.moe_route_scored(x, self.w_router, self.k, bias=self.bias, topk_idx=v["topk_idx"], topk_w=v["topk_w"],
+                              workspace=v["route_ws"], stream=stream, **self.routing)
+        moeq.moe_permute(v["topk_idx"], self.E, out=dict(v, x_perm=None), status=v["status"], workspace=v["perm_ws"],
+                         stream=stream)
+        moeq.moe_mx_quantize(x, inv_perm=v["inv_perm"], k=self.k, codes=v["codes"], scales=v["scales"],
+                             status=v["status"], stream=stream)
+        moeq.moe_grouped_ffn_mx(v["codes"], v["scales"], v["offsets"], self.blobs, self.F, workspace=v["workspace"],
+                                y_perm=v["y_perm"], status=v["status"], stream=stream)
+        return moeq.moe_unpermute_combine(v["y_perm"], v["inv_perm"], v["topk_w"], residual=residual, y=v["y"],
+                                          stream=stream)

@@ -20,6 +20,8 @@ HEADER = os.path.join(os.path.dirname(HERE), "include", "moeq.h")
 
 LAYOUT_INT4 = 0
 LAYOUT_PLANES = 1
+SCORE_SOFTMAX = 0
+SCORE_SIGMOID = 1
 DEV_BAD_INDEX = 1
 DEV_RANGE = 2
 DEV_TIMEOUT = 4
@@ -36,6 +38,9 @@ _SIGS = {
                               _c_p]),
     "moe_route_workspace_bytes": (_c_sz, [_c_i, _c_i, _c_i]),
     "moe_route_topk_noalloc": (_c_i, [_c_p, _c_p, _c_p, _c_p, _c_i, _c_i, _c_i, _c_i, _c_p, _c_p, _c_p]),
+    "moe_route_scored": (_c_i, [_c_p, _c_p, _c_p, _c_i, _c_i, _c_i, _c_i, _c_i, _c_i, _c_i, _c_i, _c_i,
+                                ctypes.c_double, _c_p, _c_p, _c_p, _c_sz, _c_p]),
+    "moe_route_scored_workspace_bytes": (_c_sz, [_c_i, _c_i, _c_i]),
     "moe_permute": (_c_i, [_c_p, _c_p, _c_p, _c_i, _c_i, _c_i, _c_i, _c_p, _c_p, _c_p, _c_p, _c_p,
                            _c_p, _c_p, _c_sz, _c_p]),
     "moe_permute_workspace_bytes": (_c_sz, [_c_i, _c_i, _c_i, _c_i]),
@@ -51,6 +56,15 @@ _SIGS = {
     "moe_grouped_ffn_combine": (_c_i, [_c_p, _c_p, _c_p, _c_i, _c_i, _c_i, _c_i, _c_i, _c_i, _c_i, _c_p, _c_p,
                                        _c_p, _c_p, _c_p, _c_p, _c_p, _c_sz, _c_p, _c_p]),
     "moe_ffn_combine_workspace_bytes": (_c_sz, [_c_i, _c_i, _c_i, _c_i, _c_i, _c_i]),
+    "moe_mx_matrix_bytes": (_c_sz, [_c_i, _c_i]),
+    "moe_mx_blob_bytes": (_c_sz, [_c_i, _c_i]),
+    "moe_mx_quantize": (_c_i, [_c_p, _c_i, _c_i, _c_i, _c_sz, _c_p, _c_i, _c_p, _c_p, _c_p, _c_p]),
+    "moe_mx_dequantize": (_c_i, [_c_p, _c_p, _c_i, _c_i, _c_i, _c_p, _c_p]),
+    "moe_mx_pack": (_c_i, [_c_p, _c_i, _c_i, _c_i, _c_i, _c_p, _c_p, _c_p]),
+    "moe_mx_pack_ffn": (_c_i, [_c_p, _c_p, _c_p, _c_i, _c_i, _c_i, _c_i, _c_p, _c_p, _c_p]),
+    "moe_mx_grouped_gemm": (_c_i, [_c_p, _c_p, _c_p, _c_p, _c_i, _c_i, _c_i, _c_i, _c_i, _c_p, _c_p, _c_p]),
+    "moe_grouped_ffn_mx": (_c_i, [_c_p, _c_p, _c_p, _c_p, _c_i, _c_i, _c_i, _c_i, _c_p, _c_sz, _c_p, _c_p, _c_p]),
+    "moe_ffn_mx_workspace_bytes": (_c_sz, [_c_i, _c_i]),
     "moe_slot_cache_create": (_c_i, [_c_i, _c_i, _c_sz, _c_p, _c_p, ctypes.POINTER(_c_p)]),
     "moe_slot_cache_create_planes": (_c_i, [_c_i, _c_i, _c_i, _c_i, _c_i, _c_p, _c_p, ctypes.POINTER(_c_p)]),
     "moe_slot_stage": (_c_i, [_c_p, _c_p, _c_p, _c_i, _c_p, _c_p, _c_p, _c_p]),
@@ -335,6 +349,219 @@ def moe_unpermute_combine(y_perm, inv_perm, topk_w, residual=None, y=None, strea
         _ptr(topk_w, torch.float32, "topk_w"), _ptr(residual, torch.bfloat16, "residual"), T, k, d,
         _ptr(y, torch.bfloat16, "y"), _stream(stream)))
     return y
+
+
+# ---- scored router and MXFP4 ------------------------------------------------
+
+_DTYPE = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}
+_SCORING = {"softmax": SCORE_SOFTMAX, "sigmoid": SCORE_SIGMOID}
+
+
+class _on:
+    """Runs a call with the tensors' own device current (a call's stream and
+    launches belong to it); tensors on different devices are refused."""
+
+    def __init__(self, fn, **tensors):
+        dev = None
+        for name, t in tensors.items():
+            if t is None:
+                continue
+            if not t.is_cuda:
+                raise ValueError(f"{fn}: {name} must be a CUDA tensor")
+            if dev is None:
+                dev = t.device
+            elif t.device != dev:
+                raise ValueError(f"{fn}: {name} is on {t.device}, the other tensors on {dev}")
+        self.guard = torch.cuda.device(dev) if dev.index != torch.cuda.current_device() else None
+
+    def __enter__(self):
+        if self.guard is not None:
+            self.guard.__enter__()
+
+    def __exit__(self, *exc):
+        if self.guard is not None:
+            self.guard.__exit__(*exc)
+
+
+def _sized(fn, name, t, shape):
+    if t is not None and tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{fn}: {name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+
+
+def _dtype_id(fn, name, dtype):
+    if dtype not in _DTYPE:
+        raise TypeError(f"{fn}: {name} must be float32, bfloat16 or float16, got {dtype}")
+    return _DTYPE[dtype]
+
+
+def moe_route_scored_workspace_bytes(T, d, E):
+    return int(load().moe_route_scored_workspace_bytes(T, d, E))
+
+
+def moe_route_scored(x, w_router, k, scoring="softmax", bias=None, n_groups=1, topk_groups=1, group_top=1,
+                     renorm=True, scale=1.0, topk_idx=None, topk_w=None, workspace=None, stream=None):
+    """Router with softmax or sigmoid scores, a balance bias, expert groups
+    and renormalised weights; returns (topk_idx, topk_w)."""
+    lib = load()
+    fn = "moe_route_scored"
+    if scoring not in _SCORING:
+        raise ValueError(f"{fn}: scoring must be 'softmax' or 'sigmoid', got {scoring!r}")
+    T, d = x.shape
+    E = w_router.shape[0]
+    _sized(fn, "w_router", w_router, (E, d))
+    _sized(fn, "bias", bias, (E,))
+    _sized(fn, "topk_idx", topk_idx, (T, k))
+    _sized(fn, "topk_w", topk_w, (T, k))
+    with _on(fn, x=x, w_router=w_router, bias=bias, topk_idx=topk_idx, topk_w=topk_w, workspace=workspace):
+        if topk_idx is None:
+            topk_idx = torch.empty(T, k, dtype=torch.int32, device=x.device)
+        if topk_w is None:
+            topk_w = torch.empty(T, k, dtype=torch.float32, device=x.device)
+        if workspace is None:
+            workspace = torch.empty(lib.moe_route_scored_workspace_bytes(T, d, E), dtype=torch.uint8, device=x.device)
+        _check(fn, lib.moe_route_scored(
+            _ptr(x, torch.bfloat16, "x"), _ptr(w_router, torch.float32, "w_router"), _ptr(bias, torch.float32, "bias"),
+            T, d, E, k, _SCORING[scoring], n_groups, topk_groups, group_top, int(bool(renorm)), float(scale),
+            _ptr(topk_idx, torch.int32, "topk_idx"), _ptr(topk_w, torch.float32, "topk_w"), _ptr(workspace),
+            workspace.numel() * workspace.element_size(), _stream(stream)))
+    return topk_idx, topk_w
+
+
+def moe_mx_matrix_bytes(N, K):
+    return int(load().moe_mx_matrix_bytes(N, K))
+
+
+def moe_mx_blob_bytes(d, F):
+    return int(load().moe_mx_blob_bytes(d, F))
+
+
+def moe_mx_quantize(x, inv_perm=None, k=1, codes=None, scales=None, status=None, stream=None):
+    """Rows of x (fp32, bf16 or fp16; rows may be strided) to MXFP4; with
+    inv_perm (from moe_permute) row t goes to its k places.  Returns (codes
+    uint8 [rows * k][K/2], scales uint8 [rows * k][K/32])."""
+    lib = load()
+    fn = "moe_mx_quantize"
+    rows, K = x.shape
+    dt = _dtype_id(fn, "x", x.dtype)
+    if (K > 1 and x.stride(1) != 1) or (rows > 1 and x.stride(0) < K):
+        raise ValueError(f"{fn}: x must have contiguous rows that do not overlap")
+    if inv_perm is not None and inv_perm.numel() != rows * k:
+        raise ValueError(f"{fn}: inv_perm must hold rows * k = {rows * k} places, got {inv_perm.numel()}")
+    _sized(fn, "codes", codes, (rows * k, K // 2))
+    _sized(fn, "scales", scales, (rows * k, K // 32))
+    with _on(fn, x=x, inv_perm=inv_perm, codes=codes, scales=scales, status=status):
+        if codes is None:
+            codes = torch.empty(rows * k, K // 2, dtype=torch.uint8, device=x.device)
+        if scales is None:
+            scales = torch.empty(rows * k, K // 32, dtype=torch.uint8, device=x.device)
+        _check(fn, lib.moe_mx_quantize(
+            x.data_ptr(), dt, rows, K, x.stride(0) if rows > 1 else K, _ptr(inv_perm, torch.int32, "inv_perm"), k,
+            _ptr(codes, torch.uint8, "codes"), _ptr(scales, torch.uint8, "scales"),
+            _ptr(status, torch.int32, "status"), _stream(stream)))
+    return codes, scales
+
+
+def moe_mx_dequantize(codes, scales, dtype=torch.bfloat16, out=None, stream=None):
+    """The values of MXFP4 rows, [rows][K] in bf16 or fp32 (exact)."""
+    lib = load()
+    fn = "moe_mx_dequantize"
+    rows, K = codes.shape[0], codes.shape[1] * 2
+    dt = _dtype_id(fn, "dtype", dtype)
+    _sized(fn, "scales", scales, (rows, K // 32))
+    _sized(fn, "out", out, (rows, K))
+    with _on(fn, codes=codes, scales=scales, out=out):
+        if out is None:
+            out = torch.empty(rows, K, dtype=dtype, device=codes.device)
+        _check(fn, lib.moe_mx_dequantize(_ptr(codes, torch.uint8, "codes"), _ptr(scales, torch.uint8, "scales"), rows,
+                                         K, dt, _ptr(out, dtype, "out"), _stream(stream)))
+    return out
+
+
+def moe_mx_pack(w, mats=None, status=None, stream=None):
+    """Matrices w [E][N][K] (fp32, bf16 or fp16) to MXFP4, uint8 [E][bytes]."""
+    lib = load()
+    fn = "moe_mx_pack"
+    E, N, K = w.shape
+    dt = _dtype_id(fn, "w", w.dtype)
+    nb = lib.moe_mx_matrix_bytes(N, K)
+    _sized(fn, "mats", mats, (E, nb))
+    with _on(fn, w=w, mats=mats, status=status):
+        if mats is None:
+            mats = torch.empty(E, nb, dtype=torch.uint8, device=w.device)
+        _check(fn, lib.moe_mx_pack(_ptr(w, None, "w"), dt, E, N, K, _ptr(mats, torch.uint8, "mats") or None,
+                                   _ptr(status, torch.int32, "status"), _stream(stream)))
+    return mats
+
+
+def moe_mx_pack_ffn(w_gate, w_up, w_down, blobs=None, status=None, stream=None):
+    """w_gate, w_up [E][F][d] and w_down [E][d][F] (one dtype) to FFN blobs, uint8 [E][bytes]."""
+    lib = load()
+    fn = "moe_mx_pack_ffn"
+    E, F, d = w_gate.shape
+    dt = _dtype_id(fn, "w_gate", w_gate.dtype)
+    _sized(fn, "w_up", w_up, (E, F, d))
+    _sized(fn, "w_down", w_down, (E, d, F))
+    nb = lib.moe_mx_blob_bytes(d, F)
+    _sized(fn, "blobs", blobs, (E, nb))
+    with _on(fn, w_gate=w_gate, w_up=w_up, w_down=w_down, blobs=blobs, status=status):
+        if blobs is None:
+            blobs = torch.empty(E, nb, dtype=torch.uint8, device=w_gate.device)
+        _check(fn, lib.moe_mx_pack_ffn(
+            _ptr(w_gate, None, "w_gate"), _ptr(w_up, w_gate.dtype, "w_up"), _ptr(w_down, w_gate.dtype, "w_down"), dt,
+            E, d, F, _ptr(blobs, torch.uint8, "blobs") or None, _ptr(status, torch.int32, "status"), _stream(stream)))
+    return blobs
+
+
+def _mx_args(fn, codes, scales, offsets, mats, E, nbytes):
+    rows, K = codes.shape[0], codes.shape[1] * 2
+    _sized(fn, "scales", scales, (rows, K // 32))
+    _sized(fn, "offsets", offsets, (E + 1,))
+    if nbytes and mats.shape[1:].numel() != nbytes:
+        raise ValueError(f"{fn}: the weights must hold {nbytes} bytes per expert, got {mats.shape[1:].numel()}")
+    return rows, K
+
+
+def moe_mx_grouped_gemm(codes, scales, offsets, mats, N, dtype=torch.float16, out=None, status=None, stream=None):
+    """y[p] = W_e xq[p] for the rows of each expert; returns [rows][N] in dtype."""
+    lib = load()
+    fn = "moe_mx_grouped_gemm"
+    E = mats.shape[0]
+    dt = _dtype_id(fn, "dtype", dtype)
+    rows, K = _mx_args(fn, codes, scales, offsets, mats, E, lib.moe_mx_matrix_bytes(N, codes.shape[1] * 2))
+    _sized(fn, "out", out, (rows, N))
+    with _on(fn, codes=codes, scales=scales, offsets=offsets, mats=mats, out=out, status=status):
+        if out is None:
+            out = torch.empty(rows, N, dtype=dtype, device=codes.device)
+        _check(fn, lib.moe_mx_grouped_gemm(
+            _ptr(codes, torch.uint8, "codes"), _ptr(scales, torch.uint8, "scales"),
+            _ptr(offsets, torch.int32, "offsets"), _ptr(mats, torch.uint8, "mats"), rows, E, N, K, dt,
+            _ptr(out, dtype, "out"), _ptr(status, torch.int32, "status"), _stream(stream)))
+    return out
+
+
+def moe_ffn_mx_workspace_bytes(rows, F):
+    return int(load().moe_ffn_mx_workspace_bytes(rows, F))
+
+
+def moe_grouped_ffn_mx(codes, scales, offsets, blobs, F, workspace=None, y_perm=None, status=None, stream=None):
+    """The grouped expert FFN on MXFP4 rows and blobs; returns y_perm fp16 [rows][d]."""
+    lib = load()
+    fn = "moe_grouped_ffn_mx"
+    E = blobs.shape[0]
+    rows, d = _mx_args(fn, codes, scales, offsets, blobs, E, lib.moe_mx_blob_bytes(codes.shape[1] * 2, F))
+    _sized(fn, "y_perm", y_perm, (rows, d))
+    with _on(fn, codes=codes, scales=scales, offsets=offsets, blobs=blobs, workspace=workspace, y_perm=y_perm,
+             status=status):
+        if workspace is None:
+            workspace = torch.empty(lib.moe_ffn_mx_workspace_bytes(rows, F), dtype=torch.uint8, device=codes.device)
+        if y_perm is None:
+            y_perm = torch.empty(rows, d, dtype=torch.float16, device=codes.device)
+        _check(fn, lib.moe_grouped_ffn_mx(
+            _ptr(codes, torch.uint8, "codes"), _ptr(scales, torch.uint8, "scales"),
+            _ptr(offsets, torch.int32, "offsets"), _ptr(blobs, torch.uint8, "blobs"), rows, E, d, F, _ptr(workspace),
+            workspace.numel() * workspace.element_size(), _ptr(y_perm, torch.float16, "y_perm"),
+            _ptr(status, torch.int32, "status"), _stream(stream)))
+    return y_perm
 
 
 class SlotCache:
