@@ -282,32 +282,34 @@ __global__ void __launch_bounds__(kThreads, 1) k_mx_gemm(const __grid_constant__
         ok = warp_wait(full(s), ph, abort_flag, P.status);
         if (!ok) break;
         tc_fence_after();
-        if (lane == 0) {
-          const int halves = P.K - kb * kKS > 128 ? 2 : 1;
-          const uint32_t sfa = tmem + C::SF0 + s * C::SF_COLS, sfb = sfa + 8;
-          const uint64_t da = da0 + s * (C::A_BYTES >> 4), db = db0 + s * (C::B_BYTES >> 4);
-          const uint64_t dsa = dsa0 + s * (C::SA_BYTES >> 4), dsb = dsb0 + s * (C::SB_BYTES >> 4);
-          for (int h = 0; h < halves; ++h) {
-            tc_copy_scales(sfa + 4 * h, dsa + 32 * h);
-            for (int r = 0; r < rts; ++r) tc_copy_scales(sfb + 4 * C::RT * h + 4 * r, dsb + 64 * r + 32 * h);
-          }
-          for (int h = 0; h < halves; ++h) {
-            const uint32_t fa = sfa + 4 * h, fb = sfb + 4 * C::RT * h + shift;
-            mma_mxf4(d, da + 4 * h, db + 4 * h, id0, fa, fb, (kb | h) != 0);
-            mma_mxf4(d, da + 4 * h + 2, db + 4 * h + 2, id1, fa, fb, 1u);
-          }
-          tc_commit(empty(s));
+        const uint32_t sfa = tmem + C::SF0 + s * C::SF_COLS, sfb = sfa + 8;
+        const uint64_t da = da0 + s * (C::A_BYTES >> 4), db = db0 + s * (C::B_BYTES >> 4);
+        const uint64_t dsa = dsa0 + s * (C::SA_BYTES >> 4), dsb = dsb0 + s * (C::SB_BYTES >> 4);
+        const bool two = P.K - kb * kKS > 128;
+        tc_copy_scales(sfa, dsa);
+        tc_copy_scales(sfb, dsb);
+        if (rts == 2) tc_copy_scales(sfb + 4, dsb + 64);
+        if (two) {
+          tc_copy_scales(sfa + 4, dsa + 32);
+          tc_copy_scales(sfb + 4 * C::RT, dsb + 32);
+          if (rts == 2) tc_copy_scales(sfb + 4 * C::RT + 4, dsb + 96);
         }
-        __syncwarp();
+        const uint32_t fb = sfb + shift;
+        mma_mxf4(d, da, db, id0, sfa, fb, kb != 0);
+        mma_mxf4(d, da + 2, db + 2, id1, sfa, fb, 1u);
+        if (two) {
+          mma_mxf4(d, da + 4, db + 4, id0, sfa + 4, fb + 4 * C::RT, 1u);
+          mma_mxf4(d, da + 6, db + 6, id1, sfa + 4, fb + 4 * C::RT, 1u);
+        }
+        tc_commit(empty(s));
         if (++s == C::STAGES) { s = 0; ph ^= 1; }
       }
       if (!ok) break;
-      if (lane == 0) tc_commit(acc_full(acc));
-      __syncwarp();
+      tc_commit(acc_full(acc));
       if (++acc == C::ACC) { acc = 0; aph ^= 1; }
     }
     // every product issued here completes before tensor memory is released
-    if (lane == 0) tc_commit(drain_bar);
+    tc_commit(drain_bar);
     const uint64_t t0 = global_ns();
     while (!mbar_try(drain_bar, 0, 1000u) && global_ns() - t0 < kWaitLimitNs) {}
     __syncwarp();
