@@ -15,15 +15,24 @@
 // instructions of about 128 cycles and 34 KB, which at the memory's share
 // per SM of about 23 bytes a cycle arrive in 1500.)
 //
-// Warps: 0 loads codes (TMA, 128B swizzle; the rows in boxes of 32, so that
-// a short tile does not read past its share) and weight scales (bulk copies
-// of scale tiles); 3 loads the rows' scales, which lie row by row (row
-// offsets of a bin are arbitrary, so they cannot come as tiles), and writes
-// them in tile order; 1 issues the scale copies into tensor memory and the
-// products; 4-7 are the epilogue; 2 allocates tensor memory.  Scale columns
-// belong to a pipeline stage, so a copy never meets a product that still
-// reads them.  Every wait is bounded; on a timeout the CTA raises
-// MOE_DEV_TIMEOUT, lets its copies land, frees tensor memory and returns.
+// Warps: 0 loads the weights' codes (TMA, 128B swizzle) and scales (bulk
+// copies of scale tiles); 2 the rows' codes (one box of 128 rows, or boxes of
+// 32 for a short tile); 3 the rows' scales, which lie row by row (row offsets
+// of a bin are arbitrary, so they cannot come as tiles), and writes them in
+// tile order; 1 issues the scale copies into tensor memory and the products;
+// 4-11 are the epilogue, two warps to a lane quadrant, each with every other
+// group of 64 columns.
+//
+// Tensor memory (512 columns) at 256 outputs a tile: two accumulators of 256
+// that share 48 columns, and two sets of scale columns.  The epilogue takes
+// the shared group of a tile's columns first, and the next tile's products
+// start as soon as that group is read, so they hide the rest of the
+// epilogue.  A set of scale columns is written again only after the products
+// that read it have completed (the commit of their stage).  Narrower tiles
+// have two whole accumulators and a set of scale columns per stage.
+//
+// Every wait is bounded; on a timeout the CTA raises MOE_DEV_TIMEOUT, lets its
+// copies land, frees tensor memory and returns.
 #include <cudaTypedefs.h>
 
 #include <atomic>
@@ -37,7 +46,8 @@ namespace {
 
 using namespace ptx;
 
-constexpr int kThreads = 256;
+constexpr int kThreads = 384;
+constexpr int kEpiWarps = 8;
 constexpr int kM = 128;       // rows of a tile
 constexpr int kKS = 256;      // K of a stage (128 bytes of codes)
 constexpr int kABox = 32;     // rows of one activation box
@@ -46,7 +56,8 @@ template <int NT>
 struct Cfg {
   static constexpr int RT = NT > 128 ? 2 : 1;  // 128-row scale tiles of the weight tile
   static constexpr int STAGES = NT == 256 ? 4 : NT == 128 ? 6 : 7;
-  static constexpr int ACC = NT == 256 ? 1 : 2;  // accumulator buffers
+  static constexpr int ACC1 = NT == 256 ? 208 : NT;  // first column of the second accumulator
+  static constexpr int SETS = NT == 256 ? 2 : STAGES;  // sets of scale columns
   static constexpr int A_BYTES = kM * 128;
   static constexpr int B_BYTES = NT * 128;
   static constexpr int SA_BYTES = 1024;       // two 128-K scale tiles
@@ -54,21 +65,22 @@ struct Cfg {
   static constexpr int OFF_B = STAGES * A_BYTES;
   static constexpr int OFF_SA = OFF_B + STAGES * B_BYTES;
   static constexpr int OFF_SB = OFF_SA + STAGES * SA_BYTES;
-  static constexpr int OFF_OUT = OFF_SB + STAGES * SB_BYTES;  // 4 warps x 32 rows x 128 bytes
-  static constexpr int OFF_TILE = OFF_OUT + 4 * 4096;         // int tile_start[E + 1], off[E + 1]
+  static constexpr int OFF_OUT = OFF_SB + STAGES * SB_BYTES;    // a warp: 32 rows x 64 bytes
+  static constexpr int OFF_TILE = OFF_OUT + kEpiWarps * 2048;   // int tile_start[E + 1], off[E + 1]
   static constexpr int OFF_BAR = OFF_TILE + 2 * (kMxMaxExperts + 1) * 4;
-  static constexpr int N_BARS = 2 * STAGES + 2 * ACC + 2;
+  static constexpr int N_BARS = 2 * STAGES + 4 + 2;
   static constexpr int OFF_MISC = OFF_BAR + N_BARS * 8;
   static constexpr int SMEM = OFF_MISC + 16 + 1024;
   static constexpr int SF_COLS = 8 + 8 * RT;  // scale columns of a stage
-  static constexpr int SF0 = ACC * NT;
-  static constexpr int TMEM_COLS = SF0 + STAGES * SF_COLS <= 256 ? 256 : 512;
-  static_assert(SF0 + STAGES * SF_COLS <= 512, "tensor memory");
+  static constexpr int SF0 = ACC1 + NT;
+  static constexpr int TMEM_COLS = SF0 + SETS * SF_COLS <= 256 ? 256 : 512;
+  static_assert(SF0 + SETS * SF_COLS <= 512, "tensor memory");
   static_assert(SMEM <= 232448, "shared memory");
 };
 
 struct Params {
-  CUtensorMap a;  // codes of the rows: bytes [rows][K/2]
+  CUtensorMap a;      // codes of the rows: bytes [rows][K/2], boxes of 32 rows
+  CUtensorMap a_all;  // the same, boxes of 128 rows
   CUtensorMap b;  // codes of the matrices: bytes [E][N][K/2]
   const uint8_t* a_scales;
   const uint8_t* b_scales;  // scale section of matrix 0
@@ -117,30 +129,31 @@ __global__ void __launch_bounds__(kThreads, 1) k_mx_gemm(const __grid_constant__
   const uint32_t bar0 = smem_u32(smem + C::OFF_BAR);
   auto full = [&](int i) { return bar0 + 8u * i; };
   auto empty = [&](int i) { return bar0 + 8u * (C::STAGES + i); };
-  auto acc_full = [&](int i) { return bar0 + 8u * (2 * C::STAGES + i); };
-  auto acc_empty = [&](int i) { return bar0 + 8u * (2 * C::STAGES + C::ACC + i); };
-  const uint32_t drain_bar = bar0 + 8u * (2 * C::STAGES + 2 * C::ACC);
+  // the CTA's tile i: its sums are complete; its columns that a later tile overwrites first are read
+  auto acc_full = [&](int i) { return bar0 + 8u * (2 * C::STAGES + (i & 1)); };
+  auto acc_free = [&](int i) { return bar0 + 8u * (2 * C::STAGES + 2 + (i & 1)); };
+  const uint32_t drain_bar = bar0 + 8u * (2 * C::STAGES + 4);
   const uint32_t exit_bar = drain_bar + 8u;
 
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
   const int E = P.E, NB = (P.N + NT - 1) / NT;
   const int KB = (P.K + kKS - 1) / kKS;  // stages of a tile; the last may hold 128 K
 
   if (tid == 0) {
     for (int i = 0; i < C::STAGES; ++i) {
-      mbar_init(full(i), 2);  // the codes producer, the row-scale warp
+      mbar_init(full(i), 3);  // warps 0, 2 and 3
       mbar_init(empty(i), 1);
     }
-    for (int i = 0; i < C::ACC; ++i) {
+    for (int i = 0; i < 2; ++i) {
       mbar_init(acc_full(i), 1);
-      mbar_init(acc_empty(i), 4);
+      mbar_init(acc_free(i), kEpiWarps);
     }
     mbar_init(drain_bar, 1);
     mbar_init(exit_bar, kThreads / 32);
     *abort_flag = 0;
     mbar_init_fence();
   }
-  if (warp == 2) tmem_alloc(smem_u32(tmem_slot), C::TMEM_COLS);
+  if (warp == 3) tmem_alloc(smem_u32(tmem_slot), C::TMEM_COLS);
   pdl_wait();
   pdl_trigger();
   // offsets are clamped into [0, rows]: no table can send a tile outside
@@ -180,38 +193,47 @@ __global__ void __launch_bounds__(kThreads, 1) k_mx_gemm(const __grid_constant__
   const uint32_t tmem = *tmem_slot;
   const int tiles = tile_start[E];
 
-  if (warp == 0) {
-    // ---- codes and weight scales ------------------------------------------
-    if (lane == 0) {
-      int s = 0, ph = 0;
-      bool ok = true;
-      for (int t = blockIdx.x; t < tiles && ok; t += gridDim.x) {
-        const Tile T = decode_tile<NT>(t, tile_start, off_s, E, P.N);
-        const int boxes = (T.nrows + kABox - 1) / kABox;
-        const int rts = C::RT == 2 && T.nn > 128 ? 2 : 1;
-        const uint8_t* sc = P.b_scales + static_cast<size_t>(T.e) * P.mat_stride;
-        for (int kb = 0; kb < KB; ++kb) {
-          ok = mbar_wait(empty(s), ph ^ 1, abort_flag, P.status);
-          if (!ok) break;
-          const uint32_t halves = P.K - kb * kKS > 128 ? 2 : 1;
-          mbar_expect_tx(full(s), boxes * (kABox * 128) + C::B_BYTES + rts * halves * 512);
-          const uint32_t adst = smem_u32(smem + s * C::A_BYTES);
-          for (int i = 0; i < boxes; ++i)
-            tma_load_2d(adst + i * (kABox * 128), &P.a, kb * 128, T.row0 + i * kABox, full(s));
+  if (warp == 0 || warp == 2) {
+    // ---- weights (warp 0), codes of the rows (warp 2) ------------------------
+    int s = 0, ph = 0;
+    bool ok = true;
+    for (int t = blockIdx.x; t < tiles && ok; t += gridDim.x) {
+      const Tile T = decode_tile<NT>(t, tile_start, off_s, E, P.N);
+      const int boxes = (T.nrows + kABox - 1) / kABox;
+      const bool two_rt = C::RT == 2 && T.nn > 128;
+      const uint8_t* sc = P.b_scales + static_cast<size_t>(T.e) * P.mat_stride +
+                          static_cast<size_t>(T.n0 >> 7) * (P.K / 128) * 512;
+      for (int kb = 0; kb < KB; ++kb) {
+        ok = warp_wait(empty(s), ph ^ 1, abort_flag, P.status);
+        if (!ok) break;
+        if (warp == 0) {
+          const uint32_t sb = P.K - kb * kKS > 128 ? 1024 : 512;
+          const uint32_t sdst = smem_u32(smem + C::OFF_SB + s * C::SB_BYTES);
+          elect_expect_tx(full(s), C::B_BYTES + (two_rt ? 2 * sb : sb));
           tma_load_3d(smem_u32(smem + C::OFF_B + s * C::B_BYTES), &P.b, kb * 128, T.n0, T.e, full(s));
-          for (int r = 0; r < rts; ++r)
-            bulk_load(smem_u32(smem + C::OFF_SB + s * C::SB_BYTES + r * 1024),
-                      sc + (static_cast<size_t>((T.n0 >> 7) + r) * (P.K / 128) + 2 * kb) * 512, halves * 512, full(s));
-          if (++s == C::STAGES) { s = 0; ph ^= 1; }
+          bulk_load(sdst, sc + static_cast<size_t>(kb) * 1024, sb, full(s));
+          if (two_rt)
+            bulk_load(sdst + 1024, sc + (static_cast<size_t>(P.K / 128) + 2 * kb) * 512, sb, full(s));
+        } else {
+          const uint32_t adst = smem_u32(smem + s * C::A_BYTES);
+          elect_expect_tx(full(s), boxes * (kABox * 128));
+          if (boxes == kM / kABox) {
+            tma_load_2d(adst, &P.a_all, kb * 128, T.row0, full(s));
+          } else {
+            for (int i = 0; i < boxes; ++i)
+              tma_load_2d(adst + i * (kABox * 128), &P.a, kb * 128, T.row0 + i * kABox, full(s));
+          }
         }
+        if (++s == C::STAGES) { s = 0; ph ^= 1; }
       }
-      if (!ok) {  // the copies in flight land before the CTA goes
-        const uint64_t t0 = global_ns();
-        for (int i = 0; i < C::STAGES; ++i) {
-          const int p = i < s ? ph : ph ^ 1;
-          while (!mbar_try(full(i), p, 1000u) && global_ns() - t0 < kWaitLimitNs) {}
-        }
+    }
+    if (!ok) {  // the copies in flight land before the CTA goes
+      const uint64_t t0 = global_ns();
+      for (int i = 0; i < C::STAGES; ++i) {
+        const int p = i < s ? ph : ph ^ 1;
+        while (!mbar_try(full(i), p, 1000u) && global_ns() - t0 < kWaitLimitNs) {}
       }
+      __syncwarp();
     }
   } else if (warp == 3) {
     // ---- row scales: four rows a lane, two 128-K words a stage --------------
@@ -265,34 +287,44 @@ __global__ void __launch_bounds__(kThreads, 1) k_mx_gemm(const __grid_constant__
     }
   } else if (warp == 1) {
     // ---- products -----------------------------------------------------------
-    int s = 0, ph = 0, acc = 0, aph = 0;
+    int s = 0, ph = 0, n = 0, tile = 0;
     bool ok = true;
     const uint64_t da0 = desc_sw128(smem_u32(smem)), db0 = desc_sw128(smem_u32(smem + C::OFF_B));
     const uint64_t dsa0 = desc_plain(smem_u32(smem + C::OFF_SA)), dsb0 = desc_plain(smem_u32(smem + C::OFF_SB));
-    for (int t = blockIdx.x; t < tiles && ok; t += gridDim.x) {
+    for (int t = blockIdx.x; t < tiles && ok; t += gridDim.x, ++tile) {
       const Tile T = decode_tile<NT>(t, tile_start, off_s, E, P.N);
       const uint32_t id0 = idesc_mxf4(T.nn, 0), id1 = idesc_mxf4(T.nn, 1);
-      const int rts = C::RT == 2 && T.nn > 128 ? 2 : 1;
+      const bool two_rt = C::RT == 2 && T.nn > 128;
       const uint32_t shift = NT == 64 ? (T.n0 >> 5) & 2 : 0;  // second half of a 128-row scale tile
-      ok = warp_wait(acc_empty(acc), aph ^ 1, abort_flag, P.status);
-      if (!ok) break;
+      if (NT == 256 ? tile >= 1 : tile >= 2) {
+        // the columns this tile writes: shared with the tile before, or the accumulator of two tiles ago
+        const int freed = NT == 256 ? tile - 1 : tile - 2;
+        ok = warp_wait(acc_free(freed), (freed >> 1) & 1, abort_flag, P.status);
+        if (!ok) break;
+      }
       tc_fence_after();
-      const uint32_t d = tmem + acc * NT;
-      for (int kb = 0; kb < KB; ++kb) {
+      const uint32_t d = tmem + (tile & 1) * C::ACC1;
+      for (int kb = 0; kb < KB; ++kb, ++n) {
         ok = warp_wait(full(s), ph, abort_flag, P.status);
         if (!ok) break;
+        if (C::SETS < C::STAGES && n >= C::SETS) {
+          // the products of SETS stages ago, which read this set of scale columns
+          const int so = (n - C::SETS) % C::STAGES, po = ((n - C::SETS) / C::STAGES) & 1;
+          ok = warp_wait(empty(so), po, abort_flag, P.status);
+          if (!ok) break;
+        }
         tc_fence_after();
-        const uint32_t sfa = tmem + C::SF0 + s * C::SF_COLS, sfb = sfa + 8;
+        const uint32_t sfa = tmem + C::SF0 + (C::SETS < C::STAGES ? n % C::SETS : s) * C::SF_COLS, sfb = sfa + 8;
         const uint64_t da = da0 + s * (C::A_BYTES >> 4), db = db0 + s * (C::B_BYTES >> 4);
         const uint64_t dsa = dsa0 + s * (C::SA_BYTES >> 4), dsb = dsb0 + s * (C::SB_BYTES >> 4);
         const bool two = P.K - kb * kKS > 128;
         tc_copy_scales(sfa, dsa);
         tc_copy_scales(sfb, dsb);
-        if (rts == 2) tc_copy_scales(sfb + 4, dsb + 64);
+        if (two_rt) tc_copy_scales(sfb + 4, dsb + 64);
         if (two) {
           tc_copy_scales(sfa + 4, dsa + 32);
           tc_copy_scales(sfb + 4 * C::RT, dsb + 32);
-          if (rts == 2) tc_copy_scales(sfb + 4 * C::RT + 4, dsb + 96);
+          if (two_rt) tc_copy_scales(sfb + 4 * C::RT + 4, dsb + 96);
         }
         const uint32_t fb = sfb + shift;
         mma_mxf4(d, da, db, id0, sfa, fb, kb != 0);
@@ -305,8 +337,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_mx_gemm(const __grid_constant__
         if (++s == C::STAGES) { s = 0; ph ^= 1; }
       }
       if (!ok) break;
-      tc_commit(acc_full(acc));
-      if (++acc == C::ACC) { acc = 0; aph ^= 1; }
+      tc_commit(acc_full(tile));
     }
     // every product issued here completes before tensor memory is released
     tc_commit(drain_bar);
@@ -314,26 +345,41 @@ __global__ void __launch_bounds__(kThreads, 1) k_mx_gemm(const __grid_constant__
     while (!mbar_try(drain_bar, 0, 1000u) && global_ns() - t0 < kWaitLimitNs) {}
     __syncwarp();
   } else if (warp >= 4) {
-    // ---- epilogue: lane = row of the tile, quadrant = warp % 4 ----------------
-    const int q = warp & 3;
-    int acc = 0, aph = 0;
+    // ---- epilogue: lane = row of the tile, quadrant = warp % 4; the quadrant's
+    // two warps take the even and the odd groups of 64 columns ------------------
+    const int q = warp & 3, half = (warp - 4) >> 2;
+    const int r = 32 * q + lane;
+    int tile = 0;
     bool ok = true;
-    for (int t = blockIdx.x; t < tiles && ok; t += gridDim.x) {
+    for (int t = blockIdx.x; t < tiles && ok; t += gridDim.x, ++tile) {
       const Tile T = decode_tile<NT>(t, tile_start, off_s, E, P.N);
-      ok = warp_wait(acc_full(acc), aph, abort_flag, P.status);
+      ok = warp_wait(acc_full(tile), (tile >> 1) & 1, abort_flag, P.status);
       if (!ok) break;
       tc_fence_after();
-      const uint32_t tb = tmem + (static_cast<uint32_t>(32 * q) << 16) + acc * NT;
-      const int r = 32 * q + lane;
+      const uint32_t tb = tmem + (static_cast<uint32_t>(32 * q) << 16) + (tile & 1) * C::ACC1;
       const bool live = r < T.nrows;
       const bool any = 32 * q < T.nrows;
+      const int groups = T.nn / 64;
       bool bad = false;
-      if (OUT == kMxOutSwiglu) {
-        // columns: 32 gate rows, 32 up rows, ...; each pair is one 32-block of h
-        uint8_t* hc = static_cast<uint8_t*>(P.out) + static_cast<size_t>(T.row0 + r) * (P.N / 4) + T.n0 / 4;
-        uint8_t* hs = P.out_scales + static_cast<size_t>(T.row0 + r) * (P.N / 64) + T.n0 / 64;
-        if (any) {
-          for (int c = 0; c < T.nn; c += 64) {
+      // 256 columns: the group in the shared columns is the last of the first
+      // accumulator, the first of the second; the warp that has it takes it
+      // first and then frees the columns, the other frees them at once
+      constexpr bool kShared = NT == 256;
+      const bool last_first = kShared && (tile & 1) == 0;
+      auto freed = [&] {
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(acc_free(tile));
+      };
+      if (kShared && half != (last_first ? 1 : 0)) freed();
+      for (int i = half; i < NT / 64; i += 2) {
+        const int grp = last_first && half == 1 ? 4 - i : i;
+        const int c = grp * 64;
+        if (grp < groups && any) {
+          if (OUT == kMxOutSwiglu) {
+            // 32 gate columns and the 32 up columns of the same features: one 32-block of h
+            uint8_t* hc = static_cast<uint8_t*>(P.out) + static_cast<size_t>(T.row0 + r) * (P.N / 4) + (T.n0 + c) / 4;
+            uint8_t* hs = P.out_scales + static_cast<size_t>(T.row0 + r) * (P.N / 64) + (T.n0 + c) / 64;
             uint32_t g[32], u[32];
             tmem_ld32(tb + c, g);
             tmem_ld32(tb + c + 32, u);
@@ -341,96 +387,90 @@ __global__ void __launch_bounds__(kThreads, 1) k_mx_gemm(const __grid_constant__
             float h[32];
             uint32_t m = 0;
 #pragma unroll
-            for (int i = 0; i < 32; ++i) {
+            for (int j = 0; j < 32; ++j) {
               // (a fast division, 2 ulp: the exact one's path for tiny operands, which the rows
               // past the tile's hold, took 4 times as long as all the rest of the kernel)
-              const float gv = __uint_as_float(g[i]);
-              h[i] = __fdividef(gv, 1.0f + __expf(-gv)) * __uint_as_float(u[i]);
-              m = max(m, __float_as_uint(h[i]) & 0x7FFFFFFFu);
+              const float gv = __uint_as_float(g[j]);
+              h[j] = __fdividef(gv, 1.0f + __expf(-gv)) * __uint_as_float(u[j]);
+              m = max(m, __float_as_uint(h[j]) & 0x7FFFFFFFu);
             }
             const uint32_t byte = mx_scale_byte(m);
             uint32_t w[4] = {0, 0, 0, 0};
             if (byte != 255u) {
               const float inv = mx_inv_scale(byte);
 #pragma unroll
-              for (int i = 0; i < 4; ++i) {
+              for (int k = 0; k < 4; ++k) {
                 float v[8];
 #pragma unroll
-                for (int j = 0; j < 8; ++j) v[j] = h[8 * i + j] * inv;
-                w[i] = mx_encode8(v);
+                for (int j = 0; j < 8; ++j) v[j] = h[8 * k + j] * inv;
+                w[k] = mx_encode8(v);
               }
             }
             if (live) {
               bad |= byte == 255u;
-              *reinterpret_cast<uint4*>(hc + c / 4) = make_uint4(w[0], w[1], w[2], w[3]);
-              hs[c / 64] = static_cast<uint8_t>(byte);
+              *reinterpret_cast<uint4*>(hc) = make_uint4(w[0], w[1], w[2], w[3]);
+              *hs = static_cast<uint8_t>(byte);
             }
-          }
-        }
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(acc_empty(acc));
-      } else {
-        // 128 bytes of every row at a time through the warp's staging rows
-        // (16-byte pieces XOR-swizzled by row), so that a store instruction
-        // covers four whole 128-byte runs
-        constexpr int ES = OUT == kMxOutF32 ? 4 : 2, CW = 128 / ES;
-        uint8_t* st = smem + C::OFF_OUT + q * 4096;
-        uint8_t* out = static_cast<uint8_t*>(P.out);
-        if (any) {
-          for (int c = 0; c < T.nn; c += CW) {
-            uint32_t v[CW / 32][32];
-#pragma unroll
-            for (int i = 0; i < CW / 32; ++i) tmem_ld32(tb + c + 32 * i, v[i]);
+          } else {
+            // 64 bytes of every row at a time through the warp's staging rows
+            // (16-byte pieces swizzled by row), so that a store instruction
+            // covers eight whole 64-byte runs
+            constexpr int ES = OUT == kMxOutF32 ? 4 : 2, CW = 64 / ES;
+            uint8_t* st = smem + C::OFF_OUT + (warp - 4) * 2048;
+            uint32_t v[64];
+            tmem_ld32(tb + c, *reinterpret_cast<uint32_t(*)[32]>(v));
+            tmem_ld32(tb + c + 32, *reinterpret_cast<uint32_t(*)[32]>(v + 32));
             tmem_ld_wait();
-            __syncwarp();  // the rows staged before have been read
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
-              uint32_t w[4];
+            for (int c1 = 0; c1 < 64; c1 += CW) {
+              __syncwarp();  // the rows staged before have been read
 #pragma unroll
-              for (int i = 0; i < 4; ++i) {
-                if (OUT == kMxOutF32) {
-                  w[i] = v[0][4 * j + i];
-                } else {
-                  const int at = 8 * j + 2 * i;
-                  const float y0 = __uint_as_float(v[at / 32][at % 32]), y1 = __uint_as_float(v[at / 32][at % 32 + 1]);
-                  if (OUT == kMxOutF16) {
-                    bad |= !(fmaxf(fabsf(y0), fabsf(y1)) <= 65504.0f) || y0 != y0 || y1 != y1;
-                    const __half2 h = __floats2half2_rn(y0, y1);
-                    w[i] = *reinterpret_cast<const uint32_t*>(&h);
+              for (int j = 0; j < 4; ++j) {
+                uint32_t w[4];
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                  if (OUT == kMxOutF32) {
+                    w[k] = v[c1 + 4 * j + k];
                   } else {
-                    const __nv_bfloat162 h = __floats2bfloat162_rn(y0, y1);
-                    w[i] = *reinterpret_cast<const uint32_t*>(&h);
+                    const float y0 = __uint_as_float(v[c1 + 8 * j + 2 * k]);
+                    const float y1 = __uint_as_float(v[c1 + 8 * j + 2 * k + 1]);
+                    if (OUT == kMxOutF16) {
+                      bad |= !(fabsf(y0) <= 65504.0f) || !(fabsf(y1) <= 65504.0f);
+                      const __half2 h = __floats2half2_rn(y0, y1);
+                      w[k] = *reinterpret_cast<const uint32_t*>(&h);
+                    } else {
+                      const __nv_bfloat162 h = __floats2bfloat162_rn(y0, y1);
+                      w[k] = *reinterpret_cast<const uint32_t*>(&h);
+                    }
                   }
                 }
+                *reinterpret_cast<uint4*>(st + lane * 64 + ((j ^ ((lane >> 1) & 3)) << 4)) =
+                    make_uint4(w[0], w[1], w[2], w[3]);
               }
-              *reinterpret_cast<uint4*>(st + lane * 128 + ((j ^ (lane & 7)) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
-            }
-            __syncwarp();
+              __syncwarp();
+              uint8_t* out = static_cast<uint8_t*>(P.out) +
+                             (static_cast<size_t>(T.row0 + 32 * q) * P.N + T.n0 + c + c1) * ES + (lane & 3) * 16;
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-              const int row = 4 * i + (lane >> 3), j = lane & 7;
-              if (32 * q + row < T.nrows)
-                *reinterpret_cast<uint4*>(out + (static_cast<size_t>(T.row0 + 32 * q + row) * P.N + T.n0 + c) * ES +
-                                          j * 16) =
-                    *reinterpret_cast<const uint4*>(st + row * 128 + ((j ^ (row & 7)) << 4));
+              for (int k = 0; k < 4; ++k) {
+                const int row = 8 * k + (lane >> 2);
+                if (32 * q + row < T.nrows)
+                  *reinterpret_cast<uint4*>(out + static_cast<size_t>(row) * P.N * ES) =
+                      *reinterpret_cast<const uint4*>(st + row * 64 + (((lane & 3) ^ ((row >> 1) & 3)) << 4));
+              }
             }
           }
         }
-        bad = bad && live;
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(acc_empty(acc));
+        if (kShared && i == half && half == (last_first ? 1 : 0)) freed();
       }
-      if (bad) flag_status(P.status, MOE_DEV_RANGE);
-      if (++acc == C::ACC) { acc = 0; aph ^= 1; }
+      if (!kShared) freed();
+      if (bad && live) flag_status(P.status, MOE_DEV_RANGE);
     }
   }
 
   __syncwarp();
   tc_fence_before();
   if (lane == 0) mbar_arrive(exit_bar);
-  if (warp == 2) {  // frees tensor memory once every warp has left its loop
+  if (warp == 3) {  // frees tensor memory once every warp has left its loop
     const uint64_t t0 = global_ns();
     while (!mbar_try(exit_bar, 0, 1000u) && global_ns() - t0 < 2 * kWaitLimitNs) {}
     __syncwarp();
@@ -475,7 +515,9 @@ moe_status_t launch(const MxGemmArgs& a, cudaStream_t s) {
                                 static_cast<cuuint64_t>(a.E)};
     const cuuint64_t strb[2] = {static_cast<cuuint64_t>(a.K / 2), static_cast<cuuint64_t>(a.mat_stride)};
     const cuuint32_t boxb[3] = {128, NT, 1};
-    if (!encode_bytes(&P.a, 2, a.a_codes, dims, str, box) || !encode_bytes(&P.b, 3, a.mats, dimb, strb, boxb)) {
+    const cuuint32_t box_all[2] = {128, kM};
+    if (!encode_bytes(&P.a, 2, a.a_codes, dims, str, box) || !encode_bytes(&P.a_all, 2, a.a_codes, dims, str, box_all) ||
+        !encode_bytes(&P.b, 3, a.mats, dimb, strb, boxb)) {
       set_error("tensor map (MXFP4 codes) could not be encoded");
       return MOE_ERR_CUDA;
     }
