@@ -116,10 +116,11 @@ def open_library(path: str = LIB_PATH) -> ctypes.CDLL:
 def load():
     """The library, for compute calls; raises without a CUDA device."""
     global _lib
+    if _lib is not None:
+        return _lib
     if not torch.cuda.is_available():
         raise RuntimeError("moeq needs a CUDA device (B200, sm_100a); no CPU fallback exists")
-    if _lib is None:
-        _lib = open_library()
+    _lib = open_library()
     return _lib
 
 
@@ -140,9 +141,17 @@ def _ptr(t, dtype=None, name="tensor"):
     return t.data_ptr()
 
 
+# The current stream's handle without a Stream object around it (3 us of a
+# decode step's host time for every call).
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
 def _stream(stream):
-    s = stream if stream is not None else torch.cuda.current_stream()
-    return s.cuda_stream
+    if stream is not None:
+        return stream.cuda_stream
+    if _raw_stream is None:
+        return torch.cuda.current_stream().cuda_stream
+    return _raw_stream(torch.cuda.current_device())
 
 
 def moe_blob_bytes(d, F, group, layout):
@@ -352,40 +361,58 @@ def moe_unpermute_combine(y_perm, inv_perm, topk_w, residual=None, y=None, strea
 
 
 # ---- scored router and MXFP4 ------------------------------------------------
+#
+# A decode step's calls are bound by the host, so the checks here are few and
+# cheap (the sizes that only the library knows are checked there).
 
 _DTYPE = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}
 _SCORING = {"softmax": SCORE_SOFTMAX, "sigmoid": SCORE_SIGMOID}
 
 
-class _on:
-    """Runs a call with the tensors' own device current (a call's stream and
-    launches belong to it); tensors on different devices are refused."""
+class _Other:
+    """Runs a call with another device current (a call's launches belong to
+    the current one)."""
 
-    def __init__(self, fn, **tensors):
-        dev = None
-        for name, t in tensors.items():
-            if t is None:
-                continue
-            if not t.is_cuda:
-                raise ValueError(f"{fn}: {name} must be a CUDA tensor")
-            if dev is None:
-                dev = t.device
-            elif t.device != dev:
-                raise ValueError(f"{fn}: {name} is on {t.device}, the other tensors on {dev}")
-        self.guard = torch.cuda.device(dev) if dev.index != torch.cuda.current_device() else None
+    __slots__ = ("guard",)
+
+    def __init__(self, device):
+        self.guard = torch.cuda.device(device)
 
     def __enter__(self):
-        if self.guard is not None:
-            self.guard.__enter__()
+        self.guard.__enter__()
 
     def __exit__(self, *exc):
-        if self.guard is not None:
-            self.guard.__exit__(*exc)
+        self.guard.__exit__(*exc)
+
+
+class _Same:
+    __slots__ = ()
+
+    def __enter__(self):
+        pass
+
+    def __exit__(self, *exc):
+        pass
+
+
+_SAME = _Same()
+
+
+def _on(fn, first, *others):
+    """A context in which the tensors' own device is current; tensors on
+    different devices are refused."""
+    dev = first.get_device()
+    if dev < 0:
+        raise ValueError(f"{fn}: the tensors must be on a CUDA device")
+    for t in others:
+        if t is not None and t.get_device() != dev:
+            raise ValueError(f"{fn}: tensors on {first.device} and {t.device}")
+    return _SAME if dev == torch.cuda.current_device() else _Other(dev)
 
 
 def _sized(fn, name, t, shape):
-    if t is not None and tuple(t.shape) != tuple(shape):
-        raise ValueError(f"{fn}: {name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    if t is not None and t.shape != shape:
+        raise ValueError(f"{fn}: {name} must have shape {shape}, got {tuple(t.shape)}")
 
 
 def _dtype_id(fn, name, dtype):
@@ -412,16 +439,16 @@ def moe_route_scored(x, w_router, k, scoring="softmax", bias=None, n_groups=1, t
     _sized(fn, "bias", bias, (E,))
     _sized(fn, "topk_idx", topk_idx, (T, k))
     _sized(fn, "topk_w", topk_w, (T, k))
-    with _on(fn, x=x, w_router=w_router, bias=bias, topk_idx=topk_idx, topk_w=topk_w, workspace=workspace):
+    with _on(fn, x, w_router, bias, topk_idx, topk_w, workspace):
         if topk_idx is None:
-            topk_idx = torch.empty(T, k, dtype=torch.int32, device=x.device)
+            topk_idx = x.new_empty((T, k), dtype=torch.int32)
         if topk_w is None:
-            topk_w = torch.empty(T, k, dtype=torch.float32, device=x.device)
+            topk_w = x.new_empty((T, k), dtype=torch.float32)
         if workspace is None:
-            workspace = torch.empty(lib.moe_route_scored_workspace_bytes(T, d, E), dtype=torch.uint8, device=x.device)
+            workspace = x.new_empty((lib.moe_route_scored_workspace_bytes(T, d, E),), dtype=torch.uint8)
         _check(fn, lib.moe_route_scored(
             _ptr(x, torch.bfloat16, "x"), _ptr(w_router, torch.float32, "w_router"), _ptr(bias, torch.float32, "bias"),
-            T, d, E, k, _SCORING[scoring], n_groups, topk_groups, group_top, int(bool(renorm)), float(scale),
+            T, d, E, k, _SCORING[scoring], n_groups, topk_groups, group_top, 1 if renorm else 0, scale,
             _ptr(topk_idx, torch.int32, "topk_idx"), _ptr(topk_w, torch.float32, "topk_w"), _ptr(workspace),
             workspace.numel() * workspace.element_size(), _stream(stream)))
     return topk_idx, topk_w
@@ -442,20 +469,23 @@ def moe_mx_quantize(x, inv_perm=None, k=1, codes=None, scales=None, status=None,
     lib = load()
     fn = "moe_mx_quantize"
     rows, K = x.shape
+    ld, step = x.stride()
     dt = _dtype_id(fn, "x", x.dtype)
-    if (K > 1 and x.stride(1) != 1) or (rows > 1 and x.stride(0) < K):
+    if rows <= 1:
+        ld = K
+    if (K > 1 and step != 1) or ld < K:
         raise ValueError(f"{fn}: x must have contiguous rows that do not overlap")
     if inv_perm is not None and inv_perm.numel() != rows * k:
         raise ValueError(f"{fn}: inv_perm must hold rows * k = {rows * k} places, got {inv_perm.numel()}")
     _sized(fn, "codes", codes, (rows * k, K // 2))
     _sized(fn, "scales", scales, (rows * k, K // 32))
-    with _on(fn, x=x, inv_perm=inv_perm, codes=codes, scales=scales, status=status):
+    with _on(fn, x, inv_perm, codes, scales, status):
         if codes is None:
-            codes = torch.empty(rows * k, K // 2, dtype=torch.uint8, device=x.device)
+            codes = x.new_empty((rows * k, K // 2), dtype=torch.uint8)
         if scales is None:
-            scales = torch.empty(rows * k, K // 32, dtype=torch.uint8, device=x.device)
+            scales = x.new_empty((rows * k, K // 32), dtype=torch.uint8)
         _check(fn, lib.moe_mx_quantize(
-            x.data_ptr(), dt, rows, K, x.stride(0) if rows > 1 else K, _ptr(inv_perm, torch.int32, "inv_perm"), k,
+            x.data_ptr(), dt, rows, K, ld, _ptr(inv_perm, torch.int32, "inv_perm"), k,
             _ptr(codes, torch.uint8, "codes"), _ptr(scales, torch.uint8, "scales"),
             _ptr(status, torch.int32, "status"), _stream(stream)))
     return codes, scales
@@ -465,13 +495,14 @@ def moe_mx_dequantize(codes, scales, dtype=torch.bfloat16, out=None, stream=None
     """The values of MXFP4 rows, [rows][K] in bf16 or fp32 (exact)."""
     lib = load()
     fn = "moe_mx_dequantize"
-    rows, K = codes.shape[0], codes.shape[1] * 2
+    rows, K = codes.shape
+    K *= 2
     dt = _dtype_id(fn, "dtype", dtype)
     _sized(fn, "scales", scales, (rows, K // 32))
     _sized(fn, "out", out, (rows, K))
-    with _on(fn, codes=codes, scales=scales, out=out):
+    with _on(fn, codes, scales, out):
         if out is None:
-            out = torch.empty(rows, K, dtype=dtype, device=codes.device)
+            out = codes.new_empty((rows, K), dtype=dtype)
         _check(fn, lib.moe_mx_dequantize(_ptr(codes, torch.uint8, "codes"), _ptr(scales, torch.uint8, "scales"), rows,
                                          K, dt, _ptr(out, dtype, "out"), _stream(stream)))
     return out
@@ -485,9 +516,9 @@ def moe_mx_pack(w, mats=None, status=None, stream=None):
     dt = _dtype_id(fn, "w", w.dtype)
     nb = lib.moe_mx_matrix_bytes(N, K)
     _sized(fn, "mats", mats, (E, nb))
-    with _on(fn, w=w, mats=mats, status=status):
+    with _on(fn, w, mats, status):
         if mats is None:
-            mats = torch.empty(E, nb, dtype=torch.uint8, device=w.device)
+            mats = w.new_empty((E, nb), dtype=torch.uint8)
         _check(fn, lib.moe_mx_pack(_ptr(w, None, "w"), dt, E, N, K, _ptr(mats, torch.uint8, "mats") or None,
                                    _ptr(status, torch.int32, "status"), _stream(stream)))
     return mats
@@ -503,35 +534,36 @@ def moe_mx_pack_ffn(w_gate, w_up, w_down, blobs=None, status=None, stream=None):
     _sized(fn, "w_down", w_down, (E, d, F))
     nb = lib.moe_mx_blob_bytes(d, F)
     _sized(fn, "blobs", blobs, (E, nb))
-    with _on(fn, w_gate=w_gate, w_up=w_up, w_down=w_down, blobs=blobs, status=status):
+    with _on(fn, w_gate, w_up, w_down, blobs, status):
         if blobs is None:
-            blobs = torch.empty(E, nb, dtype=torch.uint8, device=w_gate.device)
+            blobs = w_gate.new_empty((E, nb), dtype=torch.uint8)
         _check(fn, lib.moe_mx_pack_ffn(
             _ptr(w_gate, None, "w_gate"), _ptr(w_up, w_gate.dtype, "w_up"), _ptr(w_down, w_gate.dtype, "w_down"), dt,
             E, d, F, _ptr(blobs, torch.uint8, "blobs") or None, _ptr(status, torch.int32, "status"), _stream(stream)))
     return blobs
 
 
-def _mx_args(fn, codes, scales, offsets, mats, E, nbytes):
-    rows, K = codes.shape[0], codes.shape[1] * 2
+def _mx_args(fn, codes, scales, offsets, mats, nbytes):
+    rows, K = codes.shape
+    K *= 2
+    E = mats.shape[0]
     _sized(fn, "scales", scales, (rows, K // 32))
     _sized(fn, "offsets", offsets, (E + 1,))
-    if nbytes and mats.shape[1:].numel() != nbytes:
-        raise ValueError(f"{fn}: the weights must hold {nbytes} bytes per expert, got {mats.shape[1:].numel()}")
-    return rows, K
+    if nbytes and mats.numel() != E * nbytes:
+        raise ValueError(f"{fn}: the weights must hold {nbytes} bytes per expert, got {mats.numel() // max(E, 1)}")
+    return rows, K, E
 
 
 def moe_mx_grouped_gemm(codes, scales, offsets, mats, N, dtype=torch.float16, out=None, status=None, stream=None):
     """y[p] = W_e xq[p] for the rows of each expert; returns [rows][N] in dtype."""
     lib = load()
     fn = "moe_mx_grouped_gemm"
-    E = mats.shape[0]
     dt = _dtype_id(fn, "dtype", dtype)
-    rows, K = _mx_args(fn, codes, scales, offsets, mats, E, lib.moe_mx_matrix_bytes(N, codes.shape[1] * 2))
+    rows, K, E = _mx_args(fn, codes, scales, offsets, mats, lib.moe_mx_matrix_bytes(N, codes.shape[1] * 2))
     _sized(fn, "out", out, (rows, N))
-    with _on(fn, codes=codes, scales=scales, offsets=offsets, mats=mats, out=out, status=status):
+    with _on(fn, codes, scales, offsets, mats, out, status):
         if out is None:
-            out = torch.empty(rows, N, dtype=dtype, device=codes.device)
+            out = codes.new_empty((rows, N), dtype=dtype)
         _check(fn, lib.moe_mx_grouped_gemm(
             _ptr(codes, torch.uint8, "codes"), _ptr(scales, torch.uint8, "scales"),
             _ptr(offsets, torch.int32, "offsets"), _ptr(mats, torch.uint8, "mats"), rows, E, N, K, dt,
@@ -547,15 +579,13 @@ def moe_grouped_ffn_mx(codes, scales, offsets, blobs, F, workspace=None, y_perm=
     """The grouped expert FFN on MXFP4 rows and blobs; returns y_perm fp16 [rows][d]."""
     lib = load()
     fn = "moe_grouped_ffn_mx"
-    E = blobs.shape[0]
-    rows, d = _mx_args(fn, codes, scales, offsets, blobs, E, lib.moe_mx_blob_bytes(codes.shape[1] * 2, F))
+    rows, d, E = _mx_args(fn, codes, scales, offsets, blobs, lib.moe_mx_blob_bytes(codes.shape[1] * 2, F))
     _sized(fn, "y_perm", y_perm, (rows, d))
-    with _on(fn, codes=codes, scales=scales, offsets=offsets, blobs=blobs, workspace=workspace, y_perm=y_perm,
-             status=status):
+    with _on(fn, codes, scales, offsets, blobs, workspace, y_perm, status):
         if workspace is None:
-            workspace = torch.empty(lib.moe_ffn_mx_workspace_bytes(rows, F), dtype=torch.uint8, device=codes.device)
+            workspace = codes.new_empty((lib.moe_ffn_mx_workspace_bytes(rows, F),))
         if y_perm is None:
-            y_perm = torch.empty(rows, d, dtype=torch.float16, device=codes.device)
+            y_perm = codes.new_empty((rows, d), dtype=torch.float16)
         _check(fn, lib.moe_grouped_ffn_mx(
             _ptr(codes, torch.uint8, "codes"), _ptr(scales, torch.uint8, "scales"),
             _ptr(offsets, torch.int32, "offsets"), _ptr(blobs, torch.uint8, "blobs"), rows, E, d, F, _ptr(workspace),
