@@ -207,7 +207,10 @@ MOE_API moe_status_t moe_route_topk_noalloc(const void* x, const float* w_router
  *             when renorm != 0 (0 where that sum is 0), times scale; the bias
  *             does not enter.
  *   workspace >= moe_route_scored_workspace_bytes(T, d, E) bytes of device
- *             scratch, 16-byte aligned (x and w_router too).
+ *             scratch (enough for any smaller T too), 16-byte aligned (x and
+ *             w_router too).
+ *   status    device word or NULL: MOE_DEV_TIMEOUT when a bounded wait ran out
+ *             (the outputs are then undefined).
  * topk_idx and topk_w are what moe_permute and moe_unpermute_combine take.
  * Requires 1 <= k <= E <= 256, k <= 16, d % 32 == 0, n_groups <= 32 dividing
  * E, group_top experts or more to a group and k or more in the groups that
@@ -216,7 +219,7 @@ typedef enum { MOE_SCORE_SOFTMAX = 0, MOE_SCORE_SIGMOID = 1 } moe_scoring_t;
 MOE_API moe_status_t moe_route_scored(const void* x, const float* w_router, const float* bias, int T, int d, int E,
                                       int k, int scoring, int n_groups, int topk_groups, int group_top, int renorm,
                                       double scale, int32_t* topk_idx, float* topk_w, void* workspace,
-                                      size_t workspace_bytes, moe_stream_t stream);
+                                      size_t workspace_bytes, int32_t* status, moe_stream_t stream);
 MOE_API size_t moe_route_scored_workspace_bytes(int T, int d, int E);
 
 /* moe_permute -- per-expert histogram, exclusive prefix sum and stable

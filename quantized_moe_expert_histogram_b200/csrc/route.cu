@@ -562,7 +562,7 @@ moe_status_t launch_route_partials(const void* x, const float* w_router, int T, 
                                    size_t workspace_bytes, RoutePartials* out, cudaStream_t s) {
   const int splits = route_splits(T, d, E, workspace_bytes);
   const RouteWs ws = route_ws(workspace, splits, T, E);
-  *out = {ws.partial, ws.xsq, ws.wsq, splits, route_gamma(d)};
+  *out = {ws.partial, ws.xsq, ws.wsq, splits, splits, 2.0f * route_gamma(d)};
   const __nv_bfloat16* xb = static_cast<const __nv_bfloat16*>(x);
   return E <= 16 ? launch_logits<16>(xb, w_router, T, d, E, k, splits, ws, s)
                  : launch_logits<64>(xb, w_router, T, d, E, k, splits, ws, s);

@@ -32,7 +32,7 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
-constexpr int kMaxE = 256;
+constexpr int kMinCtas = 3;
 
 struct Scored {
   const __nv_bfloat16* x;
@@ -99,7 +99,7 @@ __device__ __forceinline__ auto group_score(int g, int gs, int top, F f) {
 }
 
 template <int P>
-__global__ void __launch_bounds__(kThreads) k_route_scored(const Scored A) {
+__global__ void __launch_bounds__(kThreads, kMinCtas) k_route_scored(const Scored A) {
   pdl_wait();
   pdl_trigger();
   __shared__ float c_s[kWarps][32 * P], d_s[kWarps][32 * P];  // choice values and bounds
@@ -132,10 +132,11 @@ __global__ void __launch_bounds__(kThreads) k_route_scored(const Scored A) {
         float v = 0.f, wq = 0.f;
         for (int s = 0; s < A.lg.splits; ++s) {
           v += A.lg.partial[(static_cast<size_t>(s) * T + t) * E + e];
-          wq += A.lg.wsq[static_cast<size_t>(s) * E + e];
         }
+        for (int s = 0; s < A.lg.w_splits; ++s) wq += A.lg.wsq[static_cast<size_t>(s) * E + e];
         L[m] = v;
-        D[m] = 2.0f * (A.lg.gamma * xn * sqrtf(wq) * (1.0f + 0.00390625f) + 5.9604645e-8f * fabsf(v)) + 1e-30f;
+        D[m] = A.lg.gamma * xn * sqrtf(wq) * (1.0f + 0.00390625f) + 1.2e-7f * fabsf(v) +
+                 5e-37f * (xn + sqrtf(wq)) + 1e-30f;
         d_max = fmaxf(d_max, D[m]);
         hard |= !(fabsf(v) <= 3.0e38f) || !(D[m] <= 3.0e38f);
       }
@@ -510,6 +511,9 @@ __global__ void __launch_bounds__(kThreads) k_route_scored(const Scored A) {
   }
 }
 
+// The logits' kernel: the tensor cores for batches that fill a tile's tokens.
+constexpr int kTensorT = 128;
+
 }  // namespace
 }  // namespace moeq
 
@@ -517,12 +521,16 @@ using namespace moeq;
 
 extern "C" {
 
-size_t moe_route_scored_workspace_bytes(int T, int d, int E) { return route_workspace_bytes(T, d, E); }
+size_t moe_route_scored_workspace_bytes(int T, int d, int E) {
+  if (T <= 0 || d <= 0 || E <= 0) return 256;
+  const size_t small = route_workspace_bytes(std::min(T, kTensorT - 1), d, E);
+  return T >= kTensorT ? std::max(small, route_tc_workspace_bytes(T, d, E)) : small;
+}
 
 moe_status_t moe_route_scored(const void* x, const float* w_router, const float* bias, int T, int d, int E, int k,
                               int scoring, int n_groups, int topk_groups, int group_top, int renorm, double scale,
                               int32_t* topk_idx, float* topk_w, void* workspace, size_t workspace_bytes,
-                              moe_stream_t stream) {
+                              int32_t* status, moe_stream_t stream) {
   const char* fn = "moe_route_scored";
   moe_status_t st = route_check_args(x, w_router, T, d, E, k, topk_idx, topk_w, fn);
   if (st != MOE_OK) return st;
@@ -552,7 +560,8 @@ moe_status_t moe_route_scored(const void* x, const float* w_router, const float*
   }
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   Scored A{};
-  st = launch_route_partials(x, w_router, T, d, E, k, workspace, workspace_bytes, &A.lg, s);
+  st = T >= kTensorT ? launch_route_partials_tc(x, w_router, T, d, E, workspace, status, &A.lg, s)
+                          : launch_route_partials(x, w_router, T, d, E, k, workspace, workspace_bytes, &A.lg, s);
   if (st != MOE_OK) return st;
   A.x = static_cast<const __nv_bfloat16*>(x);
   A.w = w_router;

@@ -143,7 +143,8 @@ class MxMoELayer:
             raise ValueError(f"T={T} exceeds max_tokens={self.max_tokens}")
         v = self.views(T)
         moeq.moe_route_scored(x, self.w_router, self.k, bias=self.bias, topk_idx=v["topk_idx"], topk_w=v["topk_w"],
-                              workspace=v["route_ws"], stream=stream, **self.routing)
+                              workspace=v["route_ws"], status=v["status"], stream=stream,
+                              **self.routing)
         moeq.moe_permute(v["topk_idx"], self.E, out=dict(v, x_perm=None), status=v["status"], workspace=v["perm_ws"],
                          stream=stream)
         moeq.moe_mx_quantize(x, inv_perm=v["inv_perm"], k=self.k, codes=v["codes"], scales=v["scales"],

@@ -39,7 +39,7 @@ _SIGS = {
     "moe_route_workspace_bytes": (_c_sz, [_c_i, _c_i, _c_i]),
     "moe_route_topk_noalloc": (_c_i, [_c_p, _c_p, _c_p, _c_p, _c_i, _c_i, _c_i, _c_i, _c_p, _c_p, _c_p]),
     "moe_route_scored": (_c_i, [_c_p, _c_p, _c_p, _c_i, _c_i, _c_i, _c_i, _c_i, _c_i, _c_i, _c_i, _c_i,
-                                ctypes.c_double, _c_p, _c_p, _c_p, _c_sz, _c_p]),
+                                ctypes.c_double, _c_p, _c_p, _c_p, _c_sz, _c_p, _c_p]),
     "moe_route_scored_workspace_bytes": (_c_sz, [_c_i, _c_i, _c_i]),
     "moe_permute": (_c_i, [_c_p, _c_p, _c_p, _c_i, _c_i, _c_i, _c_i, _c_p, _c_p, _c_p, _c_p, _c_p,
                            _c_p, _c_p, _c_sz, _c_p]),
@@ -426,7 +426,7 @@ def moe_route_scored_workspace_bytes(T, d, E):
 
 
 def moe_route_scored(x, w_router, k, scoring="softmax", bias=None, n_groups=1, topk_groups=1, group_top=1,
-                     renorm=True, scale=1.0, topk_idx=None, topk_w=None, workspace=None, stream=None):
+                     renorm=True, scale=1.0, topk_idx=None, topk_w=None, workspace=None, status=None, stream=None):
     """Router with softmax or sigmoid scores, a balance bias, expert groups
     and renormalised weights; returns (topk_idx, topk_w)."""
     lib = load()
@@ -439,7 +439,7 @@ def moe_route_scored(x, w_router, k, scoring="softmax", bias=None, n_groups=1, t
     _sized(fn, "bias", bias, (E,))
     _sized(fn, "topk_idx", topk_idx, (T, k))
     _sized(fn, "topk_w", topk_w, (T, k))
-    with _on(fn, x, w_router, bias, topk_idx, topk_w, workspace):
+    with _on(fn, x, w_router, bias, topk_idx, topk_w, workspace, status):
         if topk_idx is None:
             topk_idx = x.new_empty((T, k), dtype=torch.int32)
         if topk_w is None:
@@ -450,7 +450,7 @@ def moe_route_scored(x, w_router, k, scoring="softmax", bias=None, n_groups=1, t
             _ptr(x, torch.bfloat16, "x"), _ptr(w_router, torch.float32, "w_router"), _ptr(bias, torch.float32, "bias"),
             T, d, E, k, _SCORING[scoring], n_groups, topk_groups, group_top, 1 if renorm else 0, scale,
             _ptr(topk_idx, torch.int32, "topk_idx"), _ptr(topk_w, torch.float32, "topk_w"), _ptr(workspace),
-            workspace.numel() * workspace.element_size(), _stream(stream)))
+            workspace.numel() * workspace.element_size(), _ptr(status, torch.int32, "status"), _stream(stream)))
     return topk_idx, topk_w
 
 

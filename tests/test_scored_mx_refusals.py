@@ -15,7 +15,7 @@ def lib():
 
 
 def route(L, T=4, d=256, E=64, k=8, scoring=1, groups=8, kept=4, top=2, x=P, w=P, idx=P, wt=P, ws=P, ws_bytes=1 << 30):
-    return L.moe_route_scored(x, w, None, T, d, E, k, scoring, groups, kept, top, 1, 1.0, idx, wt, ws, ws_bytes, None)
+    return L.moe_route_scored(x, w, None, T, d, E, k, scoring, groups, kept, top, 1, 1.0, idx, wt, ws, ws_bytes, None, None)
 
 
 @pytest.mark.parametrize("args,code,words", [
