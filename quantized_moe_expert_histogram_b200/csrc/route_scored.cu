@@ -22,9 +22,9 @@
 //
 // Carrying the bound (u = 2^-24): sigmoid' = s (1 - s), and over an interval
 // of half width D <= 0.05 it grows by at most e^0.05 < 1.06; expf (2 ulp), the
-// sum and the division err by less than 8 u s, the bias addition by u |c|.
+// sum and the division (2 ulp each) err by less than 12 u s, the bias addition by u |c|.
 // Softmax: every numerator and the denominator err by a relative
-// 2 D_max + 4 u (|l - max|) + (E / 32 + 16) u at most, D_max <= 0.05.
+// 2 D_max + 4 u (|l - max|) + (E / 32 + 20) u at most, D_max <= 0.05.
 #include "common.cuh"
 
 namespace moeq {
@@ -32,7 +32,6 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
-constexpr int kMinCtas = 3;
 
 struct Scored {
   const __nv_bfloat16* x;
@@ -47,29 +46,44 @@ struct Scored {
   float* out_w;
 };
 
+// A warp's token in shared memory.
+template <int P>
+struct Row {
+  float l[32 * P], c[32 * P], d[32 * P];  // fp32 logits, choice values and their bounds
+  double v[32 * P];                       // fp64: logits (raw rows) or choice values of the refined experts
+  uint8_t cand[32 * P];                   // experts to refine; later the experts left out that may come in
+  int n;
+  int raw;  // v holds logits
+};
+
 // NaN counts as -inf.
 __device__ __forceinline__ double ordered(double v) { return v == v ? v : -INFINITY; }
 
-// The k largest of the values v[m] (expert lane + 32 m, those with bit m of
-// `allowed`), descending, ties to the lower index; lane j < k receives pick
-// j.  There are at least k allowed experts.
-template <typename V, int P>
-__device__ __forceinline__ int pick_topk(const V (&v)[P], uint32_t allowed, int k, int lane) {
+// a before b: larger value, of equal ones the lower index.
+template <typename V>
+__device__ __forceinline__ bool before(V va, int a, V vb, int b) {
+  return va > vb || (va == vb && a < b);
+}
+
+// The k largest of v (shared memory, expert lane + 32 m for bit m of
+// `allowed`), descending, ties to the lower index; lane j < k receives pick j.
+template <int P>
+__device__ __forceinline__ int pick_slow(const double* v, uint32_t allowed, int k, int lane) {
   int mine = 0;
   for (int j = 0; j < k; ++j) {
-    V best = -INFINITY;
+    double best = -INFINITY;
     int e = 0x7fffffff;
-#pragma unroll
+#pragma unroll 1
     for (int m = 0; m < P; ++m)
-      if (((allowed >> m) & 1u) && (e == 0x7fffffff || v[m] > best)) {
-        best = v[m];
+      if (((allowed >> m) & 1u) && (e == 0x7fffffff || v[lane + 32 * m] > best)) {
+        best = v[lane + 32 * m];
         e = lane + 32 * m;
       }
-#pragma unroll
+#pragma unroll 1
     for (int o = 16; o; o >>= 1) {
-      const V ov = __shfl_xor_sync(0xffffffffu, best, o);
+      const double ov = __shfl_xor_sync(0xffffffffu, best, o);
       const int oe = __shfl_xor_sync(0xffffffffu, e, o);
-      if (oe != 0x7fffffff && (e == 0x7fffffff || ov > best || (ov == best && oe < e))) {
+      if (oe != 0x7fffffff && (e == 0x7fffffff || before(ov, oe, best, e))) {
         best = ov;
         e = oe;
       }
@@ -80,37 +94,124 @@ __device__ __forceinline__ int pick_topk(const V (&v)[P], uint32_t allowed, int 
   return mine;
 }
 
-// Group score of group g (experts g gs .. + gs - 1): the largest, or the sum
-// of the two largest, of f(e).
-template <typename F>
-__device__ __forceinline__ auto group_score(int g, int gs, int top, F f) {
-  auto a = f(g * gs);
-  decltype(a) b = -INFINITY;
-  for (int i = 1; i < gs; ++i) {
-    const auto v = f(g * gs + i);
-    if (v > a) {
-      b = a;
-      a = v;
-    } else if (v > b) {
-      b = v;
-    }
+// Two largest of a stream of values.
+struct Top2 {
+  float a = -INFINITY, b = -INFINITY;
+  __device__ __forceinline__ void add(float v) {
+    b = fmaxf(b, fminf(a, v));
+    a = fmaxf(a, v);
   }
-  return top == 2 ? a + b : a;
+  __device__ __forceinline__ void merge(int o) {
+    const float oa = __shfl_xor_sync(0xffffffffu, a, o), ob = __shfl_xor_sync(0xffffffffu, b, o);
+    add(oa);
+    add(ob);
+  }
+};
+
+// The softmax's maximum and denominator in fp64, from a raw row; a NaN among
+// the logits makes both NaN.
+template <int P>
+__device__ __forceinline__ void softmax64(const double* v, int E, int lane, double& mx, double& sum) {
+  bool nan = false;
+  mx = -INFINITY;
+#pragma unroll 1
+  for (int e = lane; e < E; e += 32) {
+    nan |= v[e] != v[e];
+    mx = fmax(mx, v[e]);
+  }
+#pragma unroll
+  for (int o = 16; o; o >>= 1) mx = fmax(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+  if (__any_sync(0xffffffffu, nan)) mx = NAN;
+  sum = 0.0;
+#pragma unroll 1
+  for (int e = lane; e < E; e += 32) sum += exp(v[e] - mx);
+#pragma unroll
+  for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
 }
 
+// A row evaluated in fp64 throughout (row.v: logits of all experts): picks
+// (lane j < k) and their scores s.
 template <int P>
-__global__ void __launch_bounds__(kThreads, kMinCtas) k_route_scored(const Scored A) {
+__device__ __noinline__ int pick_whole(const Scored& A, Row<P>& row, int lane, double& s) {
+  const int E = A.E, G = A.groups, gs = E / G;
+  double mx = 0.0, sum = 1.0;
+  if (!A.sigmoid) softmax64<P>(row.v, E, lane, mx, sum);
+  auto score = [&](double l) { return A.sigmoid ? 1.0 / (1.0 + exp(-l)) : exp(l - mx) / sum; };
+  // logits out of the way, choice values in their place
+  double l[P];
+  uint32_t allowed = 0;
+#pragma unroll
+  for (int m = 0; m < P; ++m) {
+    const int e = lane + 32 * m;
+    l[m] = 0.0;
+    if (e < E) {
+      l[m] = row.v[e];
+      allowed |= 1u << m;
+    }
+  }
+  __syncwarp();
+#pragma unroll
+  for (int m = 0; m < P; ++m) {
+    const int e = lane + 32 * m;
+    if (e < E) {
+      double c;
+      if (A.by_logits) {
+        // (a softmax row with a NaN, or an infinite maximum, is NaN throughout;
+        // a sigmoid of -inf is 0: above a NaN, which counts as -inf)
+        c = A.sigmoid || mx - mx == 0.0 ? ordered(l[m]) : -INFINITY;
+        if (A.sigmoid && l[m] == -INFINITY) c = -1.7e308;
+      } else {
+        c = ordered(score(l[m]) + (A.bias ? static_cast<double>(A.bias[e]) : 0.0));
+      }
+      row.v[e] = c;
+    }
+  }
+  __syncwarp();
+  if (A.kept < G) {
+    double gv = -INFINITY;
+    if (lane < G) {
+      double a = -INFINITY, b = -INFINITY;
+#pragma unroll 1
+      for (int i = 0; i < gs; ++i) {
+        const double v = row.v[lane * gs + i];
+        if (v > a) { b = a; a = v; } else if (v > b) { b = v; }
+      }
+      gv = ordered(A.group_top == 2 ? a + b : a);
+    }
+    int ahead = 0;
+    for (int h = 0; h < G; ++h) {
+      const double o = __shfl_sync(0xffffffffu, gv, h);
+      ahead += before(o, h, gv, lane);
+    }
+    const unsigned in = __ballot_sync(0xffffffffu, lane < G && ahead < A.kept);
+#pragma unroll
+    for (int m = 0; m < P; ++m)
+      if (((allowed >> m) & 1u) && !((in >> ((lane + 32 * m) / gs)) & 1u)) allowed &= ~(1u << m);
+  }
+  const int mine = pick_slow<P>(row.v, allowed, A.k, lane);
+  double lv = 0.0;
+#pragma unroll
+  for (int m = 0; m < P; ++m) {
+    const double o = __shfl_sync(0xffffffffu, l[m], mine & 31);
+    if ((mine >> 5) == m) lv = o;
+  }
+  s = score(lv);
+  return mine;
+}
+
+// Warp per token; P experts per lane (expert lane + 32 m).
+template <int P>
+__global__ void __launch_bounds__(kThreads, 3) k_route_scored(const __grid_constant__ Scored A) {
+  __shared__ Row<P> rows[kWarps];
   pdl_wait();
   pdl_trigger();
-  __shared__ float c_s[kWarps][32 * P], d_s[kWarps][32 * P];  // choice values and bounds
-  __shared__ double l64[kWarps][32 * P];                      // refined logits
-  __shared__ uint8_t cand[kWarps][32 * P];
-  __shared__ int n_cand[kWarps];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int T = A.T, E = A.E, k = A.k, G = A.groups, gs = E / G;
   const int t = blockIdx.x * kWarps + warp;
-  const bool grouped = A.kept < G;
-  float L[P], C[P], D[P];
+  const bool here = t < T, grouped = A.kept < G;
+  const bool alone = A.sigmoid || A.by_logits;  // an expert's choice value needs no other's logit
+  Row<P>& row = rows[warp];
+  float C[P], D[P];
   uint32_t in_range = 0, refined = 0;  // bit m: expert lane + 32 m
   bool hard = false;                   // the whole row goes to fp64
   float row_max = 0.f, row_sum = 1.f;  // softmax
@@ -118,36 +219,42 @@ __global__ void __launch_bounds__(kThreads, kMinCtas) k_route_scored(const Score
   for (int m = 0; m < P; ++m)
     if (lane + 32 * m < E) in_range |= 1u << m;
 
-  if (t < T) {
-    float xq = 0.f;
-    for (int s = 0; s < A.lg.splits; ++s) xq += A.lg.xsq[static_cast<size_t>(s) * T + t];
+  if (here) {
+    float xq = 0.f, L[P], wq[P];
+#pragma unroll
+    for (int m = 0; m < P; ++m) L[m] = wq[m] = 0.f;
+#pragma unroll 4
+    for (int s = 0; s < A.lg.splits; ++s) {
+      xq += A.lg.xsq[static_cast<size_t>(s) * T + t];
+      const float* pl = A.lg.partial + (static_cast<size_t>(s) * T + t) * E + lane;
+#pragma unroll
+      for (int m = 0; m < P; ++m)
+        if (lane + 32 * m < E) L[m] += pl[32 * m];
+    }
+#pragma unroll 4
+    for (int s = 0; s < A.lg.w_splits; ++s)
+#pragma unroll
+      for (int m = 0; m < P; ++m)
+        if (lane + 32 * m < E) wq[m] += A.lg.wsq[static_cast<size_t>(s) * E + lane + 32 * m];
     const float xn = sqrtf(xq);
-    float d_max = 0.f;
+    float d_max = 0.f, mx = -INFINITY;
 #pragma unroll
     for (int m = 0; m < P; ++m) {
-      const int e = lane + 32 * m;
-      L[m] = -INFINITY;
-      D[m] = 0.f;
-      if (e < E) {
-        float v = 0.f, wq = 0.f;
-        for (int s = 0; s < A.lg.splits; ++s) {
-          v += A.lg.partial[(static_cast<size_t>(s) * T + t) * E + e];
-        }
-        for (int s = 0; s < A.lg.w_splits; ++s) wq += A.lg.wsq[static_cast<size_t>(s) * E + e];
-        L[m] = v;
-        D[m] = A.lg.gamma * xn * sqrtf(wq) * (1.0f + 0.00390625f) + 1.2e-7f * fabsf(v) +
-                 5e-37f * (xn + sqrtf(wq)) + 1e-30f;
+      const float wn = sqrtf(wq[m]);
+      D[m] = A.lg.gamma * xn * wn * (1.0f + 0.00390625f) + 1.2e-7f * fabsf(L[m]) + 5e-37f * (xn + wn) + 1e-30f;
+      hard |= !(fabsf(L[m]) <= 3.0e38f) || !(D[m] <= 3.0e38f);
+      if (lane + 32 * m < E) {
         d_max = fmaxf(d_max, D[m]);
-        hard |= !(fabsf(v) <= 3.0e38f) || !(D[m] <= 3.0e38f);
+        mx = fmaxf(mx, L[m]);
+      } else {
+        L[m] = -INFINITY;
       }
+      row.l[lane + 32 * m] = L[m];
     }
-#pragma unroll
-    for (int o = 16; o; o >>= 1) d_max = fmaxf(d_max, __shfl_xor_sync(0xffffffffu, d_max, o));
+    // magnitudes order like their bits
+    d_max = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(d_max)));
     hard = __any_sync(0xffffffffu, hard);
     if (!A.sigmoid) {
-      float mx = -INFINITY;
-#pragma unroll
-      for (int m = 0; m < P; ++m) mx = fmaxf(mx, L[m]);
 #pragma unroll
       for (int o = 16; o; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
       float sum = 0.f;
@@ -167,335 +274,289 @@ __global__ void __launch_bounds__(kThreads, kMinCtas) k_route_scored(const Score
         const float b = A.bias ? A.bias[e] : 0.f;
         float s, ds;
         if (A.sigmoid) {
-          s = 1.0f / (1.0f + expf(-L[m]));
-          ds = 1.06f * D[m] * (s * (1.0f - s) + 2.0e-7f) + 5.0e-7f * s;
+          s = __fdividef(1.0f, 1.0f + expf(-L[m]));
+          ds = 1.06f * D[m] * (s * (1.0f - s) + 2.0e-7f) + 7.0e-7f * s;
         } else {
-          s = expf(L[m] - row_max) / row_sum;
-          ds = s * (2.2f * d_max + 2.4e-7f * (row_max - L[m]) + 6.0e-8f * (E / 32 + 16)) * 1.06f;
+          s = __fdividef(expf(L[m] - row_max), row_sum);
+          ds = s * (2.2f * d_max + 2.4e-7f * (row_max - L[m]) + 6.0e-8f * (E / 32 + 20)) * 1.06f;
         }
         wide |= !(d_max <= 0.05f) || b != b || b == INFINITY;
         C[m] = s + b;
         D[m] = C[m] == -INFINITY ? 0.f : ds + 1.2e-7f * fabsf(C[m]) + 1e-37f;
       }
-      c_s[warp][lane + 32 * m] = C[m];
-      d_s[warp][lane + 32 * m] = D[m];
+      row.c[e] = C[m];
+      row.d[e] = D[m];
     }
     hard |= __any_sync(0xffffffffu, wide);
   }
-  __syncwarp();
 
-  // fp64 logits of the experts that every token of the CTA has listed (bit m
-  // of `open`), spread over its warps; `refined` gains them
+  // fp64 evaluation of the experts that the CTA's tokens have listed (bit m
+  // of `open`), a warp to each; `refined` gains them
   auto refine = [&](uint32_t open) {
     open &= ~refined;
+    if (!__syncthreads_or(open != 0)) return;
     int n = 0;
 #pragma unroll
     for (int m = 0; m < P; ++m) {
       const unsigned bal = __ballot_sync(0xffffffffu, (open >> m) & 1u);
-      if ((open >> m) & 1u) cand[warp][n + __popc(bal & ((1u << lane) - 1u))] = static_cast<uint8_t>(lane + 32 * m);
+      if ((open >> m) & 1u) row.cand[n + __popc(bal & ((1u << lane) - 1u))] = static_cast<uint8_t>(lane + 32 * m);
       n += __popc(bal);
     }
-    if (lane == 0) n_cand[warp] = n;
+    if (lane == 0) {
+      row.n = n;
+      row.raw = A.by_logits || hard || !alone;
+    }
     __syncthreads();
     int total = 0;
-    for (int w = 0; w < kWarps; ++w) total += n_cand[w];
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) total += rows[w].n;
     for (int item = warp; item < total; item += kWarps) {
       int w = 0, r = item;
-      while (r >= n_cand[w]) r -= n_cand[w++];
-      const int tu = blockIdx.x * kWarps + w, e = cand[w][r];
-      const double v = dot_bf16_f32_fp64(A.x + static_cast<size_t>(tu) * A.d, A.w + static_cast<size_t>(e) * A.d, A.d,
-                                         lane);
-      if (lane == 0) l64[w][e] = v;
+      while (r >= rows[w].n) r -= rows[w++].n;
+      const int tu = blockIdx.x * kWarps + w, e = rows[w].cand[r];
+      double v = dot_bf16_f32_fp64(A.x + static_cast<size_t>(tu) * A.d, A.w + static_cast<size_t>(e) * A.d, A.d, lane);
+      if (!rows[w].raw) v = ordered(1.0 / (1.0 + exp(-v)) + (A.bias ? static_cast<double>(A.bias[e]) : 0.0));
+      if (lane == 0) rows[w].v[e] = v;
     }
-    __syncthreads();  // also: the lists may be rewritten
+    __syncthreads();
     refined |= open;
-  };
-  // fp64 choice value of a refined expert (sigmoid or logits; a softmax that
-  // needs its denominator is `hard` whenever it is open)
-  auto value64 = [&](int e) -> double {
-    const double l = l64[warp][e];
-    if (A.by_logits) return ordered(l);
-    return ordered(1.0 / (1.0 + exp(-l)) + (A.bias ? static_cast<double>(A.bias[e]) : 0.0));
   };
 
   // ---- which groups stay ------------------------------------------------------
   uint32_t group_in = 0, group_open = 0;  // bit g, the same in every lane
   uint32_t open = 0;
-  if (t < T && grouped && !hard) {
-    float lo = -INFINITY, up = -INFINITY, cut = 0.f;
-    if (lane < G) {
-      const float* cs = c_s[warp];
-      const float* ds = d_s[warp];
-      float a = -INFINITY, b = -INFINITY;  // two largest lower bounds
-      float ua = -INFINITY, ub = -INFINITY;
-      for (int i = 0; i < gs; ++i) {
-        const float v = cs[lane * gs + i], dv = ds[lane * gs + i];
-        const float l = v - dv, h = v + dv;
-        if (l > a) { b = a; a = l; } else if (l > b) { b = l; }
-        if (h > ua) { ub = ua; ua = h; } else if (h > ub) { ub = h; }
+  if (here && grouped && !hard) {
+    __syncwarp();
+    // 32 / lpg groups at least, lpg lanes to a group
+    const int lpg = G <= 2 ? 16 : G <= 4 ? 8 : G <= 8 ? 4 : G <= 16 ? 2 : 1;
+    const int g = lane / lpg;
+    Top2 lo2, up2;
+    if (g < G)
+      for (int i = lane % lpg; i < gs; i += lpg) {
+        const float c = row.c[g * gs + i], dv = row.d[g * gs + i];
+        lo2.add(c - dv);
+        up2.add(c + dv);
       }
-      cut = A.group_top == 2 ? b : a;
-      // outward rounding of the two sums
-      lo = A.group_top == 2 ? a + b - 1.2e-7f * (fabsf(a) + fabsf(b)) : a;
-      up = A.group_top == 2 ? ua + ub + 1.2e-7f * (fabsf(ua) + fabsf(ub)) : ua;
-      if (lo != lo) lo = -INFINITY;
+    for (int o = 1; o < lpg; o <<= 1) {
+      lo2.merge(o);
+      up2.merge(o);
+    }
+    // a sum's own rounding, outward
+    float lo = lo2.a, up = up2.a, cut = lo2.a;
+    if (A.group_top == 2) {
+      cut = lo2.b;
+      lo = lo2.a + lo2.b - 1.2e-7f * (fabsf(lo2.a) + fabsf(lo2.b));
+      up = up2.a + up2.b + 1.2e-7f * (fabsf(up2.a) + fabsf(up2.b));
+      if (lo != lo) lo = -INFINITY;  // -inf - (-inf): an empty group's
       if (up != up) up = -INFINITY;
     }
     int may = 0, sure = 0;  // groups that may, that certainly do, come before this one
     for (int h = 0; h < G; ++h) {
-      const float ol = __shfl_sync(0xffffffffu, lo, h), ou = __shfl_sync(0xffffffffu, up, h);
-      if (h != lane) {
+      const float ol = __shfl_sync(0xffffffffu, lo, h * lpg), ou = __shfl_sync(0xffffffffu, up, h * lpg);
+      if (h != g) {
         may += ou >= lo;
         sure += ol > up;
       }
     }
-    group_in = __ballot_sync(0xffffffffu, lane < G && may < A.kept);
-    group_open = __ballot_sync(0xffffffffu, lane < G && may >= A.kept && sure < A.kept);
+    for (int h = 0; h < G; ++h) {
+      const int m = __shfl_sync(0xffffffffu, may, h * lpg), u = __shfl_sync(0xffffffffu, sure, h * lpg);
+      if (m < A.kept) group_in |= 1u << h;
+      else if (u < A.kept) group_open |= 1u << h;
+    }
     if (group_open) {
-      if (!A.sigmoid && !A.by_logits) {
+      if (!alone) {
         hard = true;
       } else {
 #pragma unroll
         for (int m = 0; m < P; ++m) {
-          const int e = lane + 32 * m, g = min(e / gs, G - 1);
-          const float gc = __shfl_sync(0xffffffffu, cut, g);
-          if (e < E && ((group_open >> g) & 1u) && C[m] + D[m] >= gc) open |= 1u << m;
+          const int e = lane + 32 * m, ge = min(e / gs, G - 1);
+          const float gc = __shfl_sync(0xffffffffu, cut, ge * lpg);
+          if (e < E && ((group_open >> ge) & 1u) && C[m] + D[m] >= gc) open |= 1u << m;
         }
       }
     }
   }
+  if (!here) hard = false;
   if (hard) open = in_range;
-  if (t >= T) open = 0;
-  if (grouped || __syncthreads_or(hard)) refine(open);
-  __syncwarp();
+  refine(open);
+  if (here && group_open && !hard) {
+    // the open groups by their fp64 scores: d = -1 marks the experts refined,
+    // among which each open group's best are
+    __syncwarp();
+#pragma unroll
+    for (int m = 0; m < P; ++m)
+      if ((refined >> m) & 1u) row.d[lane + 32 * m] = -1.f;
+    __syncwarp();
+    double gv = -INFINITY;
+    if (lane < G && ((group_open >> lane) & 1u)) {
+      double a = -INFINITY, b = -INFINITY;
+#pragma unroll 1
+      for (int i = 0; i < gs; ++i) {
+        const int e = lane * gs + i;
+        if (row.d[e] < 0.f) {
+          const double v = ordered(row.v[e]);
+          if (v > a) { b = a; a = v; } else if (v > b) { b = v; }
+        }
+      }
+      gv = ordered(A.group_top == 2 ? a + b : a);
+    }
+    int ahead = 0;
+    for (int h = 0; h < G; ++h) {
+      const double o = __shfl_sync(0xffffffffu, gv, h);
+      ahead += ((group_open >> h) & 1u) && before(o, h, gv, lane);
+    }
+    const int room = A.kept - __popc(group_in);
+    group_in |= __ballot_sync(0xffffffffu, lane < G && ((group_open >> lane) & 1u) && ahead < room);
+  }
 
   // ---- the picks -----------------------------------------------------------------
-  double H[P];  // hard rows: fp64 choice values
-  double row_max64 = 0.0, row_sum64 = 1.0;
-  if (t < T && hard) {
-    if (!A.sigmoid) {
-      double mx = -INFINITY;
-      bool nan = false;
-#pragma unroll
-      for (int m = 0; m < P; ++m)
-        if ((in_range >> m) & 1u) {
-          const double l = l64[warp][lane + 32 * m];
-          nan |= l != l;
-          mx = fmax(mx, l);
-        }
-#pragma unroll
-      for (int o = 16; o; o >>= 1) mx = fmax(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-      if (__any_sync(0xffffffffu, nan)) mx = NAN;
-      double sum = 0.0;
-#pragma unroll
-      for (int m = 0; m < P; ++m)
-        if ((in_range >> m) & 1u) sum += exp(l64[warp][lane + 32 * m] - mx);
-#pragma unroll
-      for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-      row_max64 = mx;
-      row_sum64 = sum;
-    }
-#pragma unroll
-    for (int m = 0; m < P; ++m) {
-      const int e = lane + 32 * m;
-      H[m] = -INFINITY;
-      if (e < E) {
-        const double l = l64[warp][e];
-        if (A.by_logits) {
-          // (a softmax row with a NaN, or two infinities' difference, is NaN throughout)
-          // (a sigmoid of -inf is 0: above a NaN, which counts as -inf)
-          H[m] = A.sigmoid || (row_max64 - row_max64 == 0.0) ? ordered(l) : -INFINITY;
-          if (A.sigmoid && l == -INFINITY) H[m] = -1.7e308;
-        } else {
-          const double s = A.sigmoid ? 1.0 / (1.0 + exp(-l)) : exp(l - row_max64) / row_sum64;
-          H[m] = ordered(s + (A.bias ? static_cast<double>(A.bias[e]) : 0.0));
-        }
-      }
-    }
-  }
-  if (t < T && grouped) {
-    // the groups still open, or (hard rows) all of them, by their fp64 scores
-    if (hard) {
-      group_in = 0;
-      group_open = G == 32 ? 0xffffffffu : (1u << G) - 1u;
-    }
-    if (group_open) {
-      // hard rows: the values go through l64 (the row's logits are kept apart)
-      double keep[P];
-      if (hard) {
-#pragma unroll
-        for (int m = 0; m < P; ++m) keep[m] = (in_range >> m) & 1u ? l64[warp][lane + 32 * m] : 0.0;
-        __syncwarp();
-#pragma unroll
-        for (int m = 0; m < P; ++m)
-          if ((in_range >> m) & 1u) l64[warp][lane + 32 * m] = H[m];
-        __syncwarp();
-      }
-      // mark of the experts refined for the groups: a bound of -1 in d_s
-      if (!hard) {
-#pragma unroll
-        for (int m = 0; m < P; ++m)
-          if ((refined >> m) & 1u) d_s[warp][lane + 32 * m] = -1.f;
-        __syncwarp();
-      }
-      double gv = -INFINITY;
-      if (lane < G && ((group_open >> lane) & 1u)) {
-        gv = group_score(lane, gs, A.group_top, [&](int e) -> double {
-          if (hard) return l64[warp][e];
-          return d_s[warp][e] < 0.f ? value64(e) : -INFINITY;  // the others are below the group's best
-        });
-        gv = ordered(gv);
-      }
-      int before = 0;
-      for (int h = 0; h < G; ++h) {
-        const double o = __shfl_sync(0xffffffffu, gv, h);
-        if (((group_open >> h) & 1u) && (o > gv || (o == gv && h < lane))) ++before;
-      }
-      const int room = A.kept - __popc(group_in);
-      const bool stay = lane < G && ((group_open >> lane) & 1u) && before < room;
-      group_in |= __ballot_sync(0xffffffffu, stay);
-      if (hard) {
-        __syncwarp();
-#pragma unroll
-        for (int m = 0; m < P; ++m)
-          if ((in_range >> m) & 1u) l64[warp][lane + 32 * m] = keep[m];
-        __syncwarp();
-      }
-    }
-  }
   uint32_t allowed = in_range;
-  if (grouped) {
-#pragma unroll
-    for (int m = 0; m < P; ++m)
-      if (!((group_in >> min((lane + 32 * m) / gs, 31)) & 1u)) allowed &= ~(1u << m);
-  }
-  int mine = 0;
-  open = 0;
+  int mine = 0, extra = 0;  // lane j < k: pick j; experts left out that may come in
   bool again = false;
-  if (t < T && !hard) {
-    mine = pick_topk(C, allowed, k, lane);
-    // intervals of the picks, lane j holding pick j's
-    const float* cs = c_s[warp];
-    float lo = INFINITY, up = -INFINITY;
-    {
-      // bound of pick j, from its lane (d_s may hold marks)
-      float dv = 0.f;
+  open = 0;
+  if (here && !hard) {
+    if (grouped) {
+#pragma unroll
+      for (int m = 0; m < P; ++m)
+        if (!((group_in >> min((lane + 32 * m) / gs, 31)) & 1u)) allowed &= ~(1u << m);
+    }
+    uint32_t left = allowed;
+    for (int j = 0; j < k; ++j) {
+      uint32_t bk = 0;
+      int be = 0x7fffffff;
 #pragma unroll
       for (int m = 0; m < P; ++m) {
-        const float o = __shfl_sync(0xffffffffu, D[m], mine & 31);
-        if ((mine >> 5) == m) dv = o;
+        const uint32_t key = order_key(C[m]);
+        if (((left >> m) & 1u) && key > bk) {  // the lane's lowest expert on equal keys
+          bk = key;
+          be = lane + 32 * m;
+        }
       }
-      if (lane < k) {
-        lo = cs[mine] - dv;
-        up = cs[mine] + dv;
-      }
+      const uint32_t top = __reduce_max_sync(0xffffffffu, bk);
+      const int e = __reduce_min_sync(0xffffffffu, bk == top ? be : 0x7fffffff);
+      if ((e & 31) == lane) left &= ~(1u << (e >> 5));
+      if (lane == j) mine = e;
     }
-    // pick j is open when its interval meets another pick's ...
-    bool mark = false;
-    for (int i = 0; i < k; ++i) {
-      const float ol = __shfl_sync(0xffffffffu, lo, i), ou = __shfl_sync(0xffffffffu, up, i);
-      if (lane < k && i != lane) mark |= ol <= up && lo <= ou;
-    }
-    // ... or that of an expert left out
-    float lo_min = lo;
-#pragma unroll
-    for (int o = 16; o; o >>= 1) lo_min = fminf(lo_min, __shfl_xor_sync(0xffffffffu, lo_min, o));
-    float hi = -INFINITY;
-    bool any_out = false;
-    uint32_t picked = 0;
-    for (int j = 0; j < k; ++j) {
-      const int e = __shfl_sync(0xffffffffu, mine, j);
-      if ((e & 31) == lane) picked |= 1u << (e >> 5);
-    }
-#pragma unroll
-    for (int m = 0; m < P; ++m)
-      if (((allowed & ~picked) >> m) & 1u) {
-        hi = any_out ? fmaxf(hi, C[m] + D[m]) : C[m] + D[m];
-        any_out = true;
-        if (C[m] + D[m] >= lo_min) open |= 1u << m;
-      }
-    any_out = __any_sync(0xffffffffu, any_out);
-#pragma unroll
-    for (int o = 16; o; o >>= 1) hi = fmaxf(hi, __shfl_xor_sync(0xffffffffu, hi, o));
-    if (lane < k && any_out) mark |= lo <= hi;
-    unsigned marks = __ballot_sync(0xffffffffu, mark);
-    again = marks != 0;
-    while (marks) {
-      const int e = __shfl_sync(0xffffffffu, mine, __ffs(marks) - 1);
-      marks &= marks - 1;
-      if ((e & 31) == lane) open |= 1u << (e >> 5);
-    }
-    if (again && !A.sigmoid && !A.by_logits) open = in_range;
-  }
-  refine(open);
-  if (t >= T) return;
-  __syncwarp();
-  const bool whole = !hard && again && !A.sigmoid && !A.by_logits;  // softmax with a bias: now evaluated throughout
-  if (whole) {
-    double mx = -INFINITY, sum = 0.0;
-#pragma unroll
-    for (int m = 0; m < P; ++m)
-      if ((in_range >> m) & 1u) mx = fmax(mx, l64[warp][lane + 32 * m]);
-#pragma unroll
-    for (int o = 16; o; o >>= 1) mx = fmax(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-#pragma unroll
-    for (int m = 0; m < P; ++m)
-      if ((in_range >> m) & 1u) sum += exp(l64[warp][lane + 32 * m] - mx);
-#pragma unroll
-    for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    // Settled when each pick's interval lies above the next one's, and the
+    // last pick's above those of the experts left out.
+    float dv = 0.f;
 #pragma unroll
     for (int m = 0; m < P; ++m) {
-      const int e = lane + 32 * m;
-      H[m] = e < E ? ordered(exp(l64[warp][e] - mx) / sum + (A.bias ? static_cast<double>(A.bias[e]) : 0.0))
-                   : -INFINITY;
+      const float o = __shfl_sync(0xffffffffu, D[m], mine & 31);
+      if ((mine >> 5) == m) dv = o;
     }
-    row_max64 = mx;
-    row_sum64 = sum;
-  }
-  const bool exact = hard || whole;
-  if (exact) {
-    mine = pick_topk(H, allowed, k, lane);
-  } else if (again) {
+    const float lo = lane < k ? row.c[mine] - dv : INFINITY, up = lane < k ? row.c[mine] + dv : -INFINITY;
+    const float lo_prev = __shfl_up_sync(0xffffffffu, lo, 1);
+    float hi = -INFINITY;
+    bool out = false;
 #pragma unroll
     for (int m = 0; m < P; ++m)
-      H[m] = (refined >> m) & 1u ? value64(lane + 32 * m) : static_cast<double>(C[m]);
-    mine = pick_topk(H, allowed, k, lane);
+      if ((left >> m) & 1u) {
+        hi = fmaxf(hi, C[m] + D[m]);
+        out = true;
+      }
+    const float lo_last = __shfl_sync(0xffffffffu, lo, k - 1);
+    again = __any_sync(0xffffffffu, (out && hi >= lo_last) || (lane > 0 && lane < k && !(lo_prev > up)));
+    if (again && !alone) {
+      open = in_range;
+    } else if (again) {
+      float lo_min = lo;
+#pragma unroll
+      for (int o = 16; o; o >>= 1) {
+        lo_min = fminf(lo_min, __shfl_xor_sync(0xffffffffu, lo_min, o));
+        hi = fmaxf(hi, __shfl_xor_sync(0xffffffffu, hi, o));
+      }
+      // open: picks whose intervals meet another pick's or an expert's left out, and those experts
+      const bool any_out = __any_sync(0xffffffffu, out);
+      bool mark = lane < k && any_out && lo <= hi;
+      for (int i = 0; i < k; ++i) {
+        const float ol = __shfl_sync(0xffffffffu, lo, i), ou = __shfl_sync(0xffffffffu, up, i);
+        if (lane < k && i != lane) mark |= ol <= up && lo <= ou;
+      }
+      unsigned marks = __ballot_sync(0xffffffffu, mark);
+      while (marks) {
+        const int e = __shfl_sync(0xffffffffu, mine, __ffs(marks) - 1);
+        marks &= marks - 1;
+        if ((e & 31) == lane) open |= 1u << (e >> 5);
+      }
+      uint32_t in = 0;
+#pragma unroll
+      for (int m = 0; m < P; ++m)
+        if (((left >> m) & 1u) && C[m] + D[m] >= lo_min) in |= 1u << m;
+      open |= in;
+      extra = in;
+    }
+  }
+  refine(open);
+  if (!here) return;
+  __syncwarp();
+  double s64 = 0.0;
+  const bool whole = hard || (again && !alone);
+  if (whole) {
+    mine = pick_whole<P>(A, row, lane, s64);
+  } else if (again) {
+    // candidates, one to a lane: the picks, then the experts that may come in
+    // (more of them than lanes: from shared memory); values fp64 where
+    // refined, else the fp32 ones, whose intervals meet no other's
+    int n = 0;
+#pragma unroll
+    for (int m = 0; m < P; ++m) {
+      const unsigned bal = __ballot_sync(0xffffffffu, (extra >> m) & 1u);
+      if ((extra >> m) & 1u) row.cand[n + __popc(bal & ((1u << lane) - 1u))] = static_cast<uint8_t>(lane + 32 * m);
+      n += __popc(bal);
+    }
+    __syncwarp();
+    n += k;
+    if (n <= 32) {
+      const int e = lane < k ? mine : lane < n ? row.cand[lane - k] : 0;
+      bool fp64 = false;
+#pragma unroll
+      for (int m = 0; m < P; ++m) {
+        const uint32_t o = __shfl_sync(0xffffffffu, refined, e & 31);
+        if ((e >> 5) == m) fp64 = (o >> m) & 1u;
+      }
+      const double v = lane >= n ? -INFINITY : fp64 ? ordered(row.v[e]) : static_cast<double>(row.c[e]);
+      int rank = 0;
+      for (int i = 0; i < n; ++i) {
+        const double ov = __shfl_sync(0xffffffffu, v, i);
+        const int oe = __shfl_sync(0xffffffffu, e, i);
+        rank += before(ov, oe, v, e);
+      }
+      for (int j = 0; j < k; ++j) {
+        const unsigned at = __ballot_sync(0xffffffffu, lane < n && rank == j);
+        const int pe = __shfl_sync(0xffffffffu, e, __ffs(at) - 1);
+        if (lane == j) mine = pe;
+      }
+    } else {
+#pragma unroll
+      for (int m = 0; m < P; ++m) {
+        const int e = lane + 32 * m;
+        if (e < E) row.v[e] = (refined >> m) & 1u ? ordered(row.v[e]) : static_cast<double>(C[m]);
+      }
+      __syncwarp();
+      mine = pick_slow<P>(row.v, allowed, k, lane);
+    }
   }
 
   // ---- weights: lane j < k holds pick j ----------------------------------------------
-  double l = 0.0;
-#pragma unroll
-  for (int m = 0; m < P; ++m) {
-    const float o = __shfl_sync(0xffffffffu, L[m], mine & 31);
-    const bool r = (__shfl_sync(0xffffffffu, refined, mine & 31) >> m) & 1u;
-    if ((mine >> 5) == m) l = r ? l64[warp][mine] : static_cast<double>(o);
-  }
   float wt;
-  if (exact) {
-    double s = A.sigmoid ? 1.0 / (1.0 + exp(-l)) : exp(l - row_max64) / row_sum64;
+  if (whole) {
     if (A.renorm) {
-      double sum = lane < k ? s : 0.0;
+      double sum = lane < k ? s64 : 0.0;
 #pragma unroll
       for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-      s = sum == 0.0 ? 0.0 : s / sum;
+      s64 = sum == 0.0 ? 0.0 : s64 / sum;
     }
-    wt = static_cast<float>(s * A.scale);
+    wt = static_cast<float>(s64 * A.scale);
   } else {
-    const float lf = static_cast<float>(l);
-    float s = A.sigmoid ? 1.0f / (1.0f + expf(-lf)) : expf(lf - row_max);
+    const float l = row.l[mine];
+    float s = A.sigmoid ? 1.0f / (1.0f + expf(-l)) : expf(l - row_max);
     if (A.renorm) {
       // scores so small that they leave fp32's range: taken from the largest
-      float top = lane < k ? (A.sigmoid ? lf : 0.f) : -INFINITY;
+      float top = lane < k ? l : -INFINITY;
 #pragma unroll
       for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-      if (A.sigmoid && top < -60.f) {
-        s = expf(lf - top);  // sigmoid(l) = e^l (1 + tiny)
-      } else if (!A.sigmoid) {
-        float mx = lane < k ? lf : -INFINITY;
-#pragma unroll
-        for (int o = 16; o; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-        s = expf(lf - mx);
-      }
+      if (!A.sigmoid || top < -60.f) s = expf(l - top);  // (sigmoid(l) = e^l (1 + tiny))
       float sum = lane < k ? s : 0.f;
 #pragma unroll
       for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
