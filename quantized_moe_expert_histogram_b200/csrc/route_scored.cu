@@ -199,18 +199,17 @@ __device__ __noinline__ int pick_whole(const Scored& A, Row<P>& row, int lane, d
   return mine;
 }
 
-// Warp per token; P experts per lane (expert lane + 32 m).
-template <int P>
-__global__ void __launch_bounds__(kThreads, 3) k_route_scored(const __grid_constant__ Scored A) {
-  __shared__ Row<P> rows[kWarps];
-  pdl_wait();
-  pdl_trigger();
+// The tokens block * kWarps .. of a CTA, a warp to each; P experts per lane
+// (expert lane + 32 m), R rows in shared memory (the block has no more tokens).
+// load(t, L, D): the token's fp32 logits and bounds.
+template <int P, int R = kWarps, typename Load>
+__device__ __forceinline__ void select_block(const Scored& A, Row<P>* rows, int block, Load load) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int T = A.T, E = A.E, k = A.k, G = A.groups, gs = E / G;
-  const int t = blockIdx.x * kWarps + warp;
+  const int t = block * kWarps + warp;
   const bool here = t < T, grouped = A.kept < G;
   const bool alone = A.sigmoid || A.by_logits;  // an expert's choice value needs no other's logit
-  Row<P>& row = rows[warp];
+  Row<P>& row = rows[min(warp, R - 1)];  // (a warp without a token writes nothing)
   float C[P], D[P];
   uint32_t in_range = 0, refined = 0;  // bit m: expert lane + 32 m
   bool hard = false;                   // the whole row goes to fp64
@@ -220,28 +219,11 @@ __global__ void __launch_bounds__(kThreads, 3) k_route_scored(const __grid_const
     if (lane + 32 * m < E) in_range |= 1u << m;
 
   if (here) {
-    float xq = 0.f, L[P], wq[P];
-#pragma unroll
-    for (int m = 0; m < P; ++m) L[m] = wq[m] = 0.f;
-#pragma unroll 4
-    for (int s = 0; s < A.lg.splits; ++s) {
-      xq += A.lg.xsq[static_cast<size_t>(s) * T + t];
-      const float* pl = A.lg.partial + (static_cast<size_t>(s) * T + t) * E + lane;
-#pragma unroll
-      for (int m = 0; m < P; ++m)
-        if (lane + 32 * m < E) L[m] += pl[32 * m];
-    }
-#pragma unroll 4
-    for (int s = 0; s < A.lg.w_splits; ++s)
-#pragma unroll
-      for (int m = 0; m < P; ++m)
-        if (lane + 32 * m < E) wq[m] += A.lg.wsq[static_cast<size_t>(s) * E + lane + 32 * m];
-    const float xn = sqrtf(xq);
+    float L[P];
+    load(t, L, D);
     float d_max = 0.f, mx = -INFINITY;
 #pragma unroll
     for (int m = 0; m < P; ++m) {
-      const float wn = sqrtf(wq[m]);
-      D[m] = A.lg.gamma * xn * wn * (1.0f + 0.00390625f) + 1.2e-7f * fabsf(L[m]) + 5e-37f * (xn + wn) + 1e-30f;
       hard |= !(fabsf(L[m]) <= 3.0e38f) || !(D[m] <= 3.0e38f);
       if (lane + 32 * m < E) {
         d_max = fmaxf(d_max, D[m]);
@@ -302,18 +284,18 @@ __global__ void __launch_bounds__(kThreads, 3) k_route_scored(const __grid_const
       if ((open >> m) & 1u) row.cand[n + __popc(bal & ((1u << lane) - 1u))] = static_cast<uint8_t>(lane + 32 * m);
       n += __popc(bal);
     }
-    if (lane == 0) {
+    if (lane == 0 && warp < R) {
       row.n = n;
       row.raw = A.by_logits || hard || !alone;
     }
     __syncthreads();
     int total = 0;
 #pragma unroll
-    for (int w = 0; w < kWarps; ++w) total += rows[w].n;
+    for (int w = 0; w < R; ++w) total += rows[w].n;
     for (int item = warp; item < total; item += kWarps) {
       int w = 0, r = item;
       while (r >= rows[w].n) r -= rows[w++].n;
-      const int tu = blockIdx.x * kWarps + w, e = rows[w].cand[r];
+      const int tu = block * kWarps + w, e = rows[w].cand[r];
       double v = dot_bf16_f32_fp64(A.x + static_cast<size_t>(tu) * A.d, A.w + static_cast<size_t>(e) * A.d, A.d, lane);
       if (!rows[w].raw) v = ordered(1.0 / (1.0 + exp(-v)) + (A.bias ? static_cast<double>(A.bias[e]) : 0.0));
       if (lane == 0) rows[w].v[e] = v;
@@ -572,6 +554,85 @@ __global__ void __launch_bounds__(kThreads, 3) k_route_scored(const __grid_const
   }
 }
 
+template <int P>
+__global__ void __launch_bounds__(kThreads, 3) k_route_scored(const __grid_constant__ Scored A) {
+  __shared__ Row<P> rows[kWarps];
+  pdl_wait();
+  pdl_trigger();
+  select_block<P>(A, rows, blockIdx.x, [&](int t, float (&L)[P], float (&D)[P]) {
+    const int lane = threadIdx.x & 31, T = A.T, E = A.E;
+    float xq = 0.f, wq[P];
+#pragma unroll
+    for (int m = 0; m < P; ++m) L[m] = wq[m] = 0.f;
+#pragma unroll 4
+    for (int s = 0; s < A.lg.splits; ++s) {
+      xq += A.lg.xsq[static_cast<size_t>(s) * T + t];
+      const float* pl = A.lg.partial + (static_cast<size_t>(s) * T + t) * E + lane;
+#pragma unroll
+      for (int m = 0; m < P; ++m)
+        if (lane + 32 * m < E) L[m] += pl[32 * m];
+    }
+#pragma unroll 4
+    for (int s = 0; s < A.lg.w_splits; ++s)
+#pragma unroll
+      for (int m = 0; m < P; ++m)
+        if (lane + 32 * m < E) wq[m] += A.lg.wsq[static_cast<size_t>(s) * E + lane + 32 * m];
+    const float xn = sqrtf(xq);
+#pragma unroll
+    for (int m = 0; m < P; ++m) {
+      const float wn = sqrtf(wq[m]);
+      D[m] = A.lg.gamma * xn * wn * (1.0f + 0.00390625f) + 1.2e-7f * fabsf(L[m]) + 5e-37f * (xn + wn) + 1e-30f;
+    }
+  });
+}
+
+// The smallest batches: logits and selection in one launch of a thread-block
+// cluster.  A CTA sums one slice of d for all T E logits (fp32 FMA chains of
+// the products and of their magnitudes, cluster_partial_dots_f32) into CTA 0,
+// which selects:  |L - l| <= 2 cluster_gamma(d) (sum of magnitudes)(1 + 2^-8).
+constexpr int tiny_logits(int P) { return P <= 2 ? 512 : 256; }  // 48 KB of shared memory
+constexpr int tiny_rows(int P) { return P == 8 ? 1 : kWarps; }   // E > 128: 256 logits are one token's
+
+template <int P>
+__global__ void __launch_bounds__(kThreads) k_route_scored_tiny(const __grid_constant__ Scored A) {
+  __shared__ Row<P> rows[tiny_rows(P)];
+  __shared__ float2 part[kClusterSlices * tiny_logits(P)];
+  cluster_sync_start();
+  pdl_wait();
+  pdl_trigger();
+  const int rank = blockIdx.x;  // the grid is one cluster
+  const int n = A.T * A.E, dk = A.d / kClusterSlices;
+  cluster_partial_dots_f32(
+      n, rank * dk, dk,
+      [&](int i, const __nv_bfloat16*& xr, const float*& wr) {
+        const int t = i / A.E;
+        xr = A.x + static_cast<size_t>(t) * A.d;
+        wr = A.w + static_cast<size_t>(i - t * A.E) * A.d;
+      },
+      cluster_map_shared(part, 0) + 8u * static_cast<uint32_t>(rank * n));
+  cluster_sync_publish();
+  if (rank != 0) return;
+  select_block<P, tiny_rows(P)>(A, rows, 0, [&](int t, float (&L)[P], float (&D)[P]) {
+    const int lane = threadIdx.x & 31;
+#pragma unroll
+    for (int m = 0; m < P; ++m) {
+      float v = 0.f, mag = 0.f;
+      if (lane + 32 * m < A.E) {
+#pragma unroll
+        for (int r = 0; r < kClusterSlices; ++r) {
+          const float2 q = part[r * n + t * A.E + lane + 32 * m];
+          v += q.x;
+          mag += q.y;
+        }
+      }
+      L[m] = v;
+      D[m] = 2.0f * A.lg.gamma * mag * (1.0f + 0.00390625f) + 1e-30f;
+    }
+  });
+}
+
+bool tiny(int T, int d, int E) { return T <= kWarps && d % 64 == 0 && T * E <= tiny_logits(ceil_div(E, 32)); }
+
 // The logits' kernel: the tensor cores for batches that fill a tile's tokens.
 constexpr int kTensorT = 128;
 
@@ -621,7 +682,8 @@ moe_status_t moe_route_scored(const void* x, const float* w_router, const float*
   }
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   Scored A{};
-  st = T >= kTensorT ? launch_route_partials_tc(x, w_router, T, d, E, workspace, status, &A.lg, s)
+  if (!tiny(T, d, E))
+    st = T >= kTensorT ? launch_route_partials_tc(x, w_router, T, d, E, workspace, status, &A.lg, s)
                           : launch_route_partials(x, w_router, T, d, E, k, workspace, workspace_bytes, &A.lg, s);
   if (st != MOE_OK) return st;
   A.x = static_cast<const __nv_bfloat16*>(x);
@@ -640,6 +702,14 @@ moe_status_t moe_route_scored(const void* x, const float* w_router, const float*
   A.scale = static_cast<float>(scale);
   A.out_idx = topk_idx;
   A.out_w = topk_w;
+  if (tiny(T, d, E)) {
+    A.lg.gamma = cluster_gamma(d);
+    auto kern = E <= 32   ? k_route_scored_tiny<1>
+                : E <= 64 ? k_route_scored_tiny<2>
+                : E <= 128 ? k_route_scored_tiny<4>
+                           : k_route_scored_tiny<8>;
+    return cuda_check(launch_cluster_pdl(kern, kClusterSlices, dim3(kThreads), 0, s, A), "moe_route_scored launch");
+  }
   auto kern = E <= 32 ? k_route_scored<1> : E <= 64 ? k_route_scored<2> : E <= 128 ? k_route_scored<4> : k_route_scored<8>;
   return cuda_check(launch_pdl(pdl_for(static_cast<long>(T) * k), kern, dim3(ceil_div(T, kWarps)), dim3(kThreads), 0, s, A),
                     "moe_route_scored launch");

@@ -46,14 +46,17 @@ def check(x, w, k, bias=None, rtol=RTOL, **kw):
 
 
 @pytest.mark.parametrize("router", range(len(ROUTERS)))
-@pytest.mark.parametrize("T,d,E,k", [(1, 2048, 64, 8), (7, 256, 16, 2), (130, 288, 128, 6), (300, 1024, 256, 8)])
+# one cluster launch (1 to 8 tokens), fp32 logits, tensor-core logits (from 128 tokens)
+@pytest.mark.parametrize("T,d,E,k", [(1, 2048, 64, 8), (8, 1088, 64, 8), (1, 512, 256, 8), (2, 576, 128, 5), (7, 256, 16, 2),
+                                     (9, 2048, 64, 8), (127, 352, 96, 8), (130, 288, 128, 6), (300, 1024, 256, 8),
+                                     (513, 224, 160, 8)])
 def test_choice_and_weights(T, d, E, k, router):
     kw = dict(ROUTERS[router])
     x, w, b = draw(T, d, E, seed=100 + router)
     check(x, w, k, bias=b if kw.pop("bias", False) else None, **kw)
 
 
-@pytest.mark.parametrize("T", [1, 33])
+@pytest.mark.parametrize("T", [1, 33, 257])
 @pytest.mark.parametrize("E,k,G", [(60, 4, 4), (8, 8, 1), (1, 1, 1), (40, 16, 5)])
 def test_odd_expert_counts(T, E, k, G):
     x, w, b = draw(T, 64, E, seed=7, std=0.2)
@@ -62,29 +65,32 @@ def test_odd_expert_counts(T, E, k, G):
         check(x, w, k, bias=b, scoring=scoring, n_groups=G, topk_groups=kept)
 
 
+@pytest.mark.parametrize("T", [4, 40, 140])
 @pytest.mark.parametrize("router", range(len(ROUTERS)))
-def test_exact_ties_go_to_the_lower_index(router):
+def test_exact_ties_go_to_the_lower_index(router, T):
     kw = dict(ROUTERS[router])
-    x, w, b = draw(40, 512, 64, seed=8)
+    x, w, b = draw(T, 512, 64, seed=8)
     w = w[torch.arange(64) % 13]                # each row many times, across groups
     check(x, w, 8, bias=torch.zeros(64) if kw.pop("bias", False) else None, **kw)
 
 
+@pytest.mark.parametrize("T", [6, 60, 150])
 @pytest.mark.parametrize("router", range(len(ROUTERS)))
-def test_near_ties(router):
+def test_near_ties(router, T):
     """Rows that differ in their last fp32 bits: closer than the fp32 sums'
     error, apart in fp64."""
     kw = dict(ROUTERS[router])
-    x, w, b = draw(60, 1024, 64, seed=9)
+    x, w, b = draw(T, 1024, 64, seed=9)
     w = w[torch.arange(64) % 8].clone()
     w.view(torch.int32)[:, ::7] += torch.arange(64, dtype=torch.int32)[:, None] % 5
     check(x, w, 8, bias=b[torch.arange(64) % 8] if kw.pop("bias", False) else None, **kw)
 
 
+@pytest.mark.parametrize("T", [3, 21, 129])
 @pytest.mark.parametrize("scoring", ["softmax", "sigmoid"])
 @pytest.mark.parametrize("G,kept,top", [(1, 1, 1), (4, 2, 1), (4, 2, 2)])
-def test_masked_experts(scoring, G, kept, top):
-    x, w, b = draw(21, 256, 32, seed=10)
+def test_masked_experts(scoring, G, kept, top, T):
+    x, w, b = draw(T, 256, 32, seed=10)
     kw = dict(scoring=scoring, n_groups=G, topk_groups=kept, group_top=top)
     b[[0, 3, 9, 17, 30]] = -float("inf")
     ref = check(x, w, 4, bias=b, **kw)
@@ -97,10 +103,11 @@ def test_masked_experts(scoring, G, kept, top):
     check(x, w, 4, bias=b, **kw)
 
 
+@pytest.mark.parametrize("T", [6, 20, 131])
 @pytest.mark.parametrize("scoring", ["softmax", "sigmoid"])
 @pytest.mark.parametrize("bias", [False, True])
-def test_rows_that_are_not_finite(scoring, bias):
-    x, w, b = draw(6, 128, 16, seed=11)
+def test_rows_that_are_not_finite(scoring, bias, T):
+    x, w, b = draw(T, 128, 16, seed=11)
     x[1, 5] = float("inf")
     x[2, 5] = float("nan")
     x[3, 7], x[3, 8] = float("inf"), -float("inf")
@@ -110,9 +117,10 @@ def test_rows_that_are_not_finite(scoring, bias):
         check(x, w, 3, bias=b if bias else None, scoring=scoring, n_groups=G, topk_groups=kept, group_top=top)
 
 
-def test_far_scores():
+@pytest.mark.parametrize("T", [2, 12, 140])
+def test_far_scores(T):
     """Sigmoid scores that leave fp32's range, and saturated ones."""
-    x, w, b = draw(12, 256, 32, seed=12)
+    x, w, b = draw(T, 256, 32, seed=12)
     x[:, 0] = 1.0
     w[:, 0] = -120.0
     # scores of about e^-120: the logits' fp32 rounding (120 x 2^-24 x a few) is what the weights show
@@ -120,6 +128,28 @@ def test_far_scores():
     check(x, w, 4, scoring="sigmoid", bias=b, rtol=2e-4)
     w[:, 0] = 30.0
     check(x, w, 4, scoring="sigmoid", bias=b)
+
+
+@pytest.mark.parametrize("T,d,E", [(200, 2048, 256), (64, 1024, 64)])
+def test_logit_bounds_hold(T, d, E):
+    """Weights of very different magnitudes along a row, sums that cancel:
+    the choice stays that of the fp64 scores (it would not if the error
+    bounds were too small)."""
+    x, w, _ = draw(T, d, E, seed=14)
+    w = w * torch.exp2(torch.randint(-12, 8, (1, d), generator=torch.Generator().manual_seed(15)).float())
+    x[:, 1::2] = x[:, 0::2]
+    w[:, 1::2] = -w[:, 0::2] * (1 + 2.0 ** -12 * torch.randn(E, d // 2, generator=torch.Generator().manual_seed(16)))
+    for kw in (dict(), dict(scoring="sigmoid"), dict(scoring="sigmoid", bias=torch.linspace(-1e-4, 1e-4, E)),
+               dict(scoring="sigmoid", n_groups=8, topk_groups=3, group_top=2)):
+        # sums of terms of magnitude about 2^7 that cancel to about 1e-2: relative to the
+        # weights, fp32's rounding shows
+        check(x, w, 8, rtol=2e-2, **kw)
+
+
+def test_workspace_of_the_largest_batch_serves_the_smaller():
+    for d, E in ((256, 64), (2048, 256), (64, 8)):
+        sizes = [moeq.moe_route_scored_workspace_bytes(T, d, E) for T in (1, 7, 8, 100, 127, 128, 129, 1000, 4096, 5000, 70000)]
+        assert sizes == sorted(sizes)
 
 
 def test_outputs_workspace_and_refusals():
