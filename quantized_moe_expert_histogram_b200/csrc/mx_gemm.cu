@@ -33,13 +33,9 @@
 //
 // Every wait is bounded; on a timeout the CTA raises MOE_DEV_TIMEOUT, lets its
 // copies land, frees tensor memory and returns.
-#include <cudaTypedefs.h>
-
 #include <atomic>
-#include <mutex>
 
-#include "mx.cuh"
-#include "ptx.cuh"
+#include "mx_gemm.cuh"
 
 namespace moeq {
 namespace {
@@ -47,10 +43,8 @@ namespace {
 using namespace ptx;
 
 constexpr int kThreads = 384;
-constexpr int kEpiWarps = 8;
 constexpr int kM = 128;       // rows of a tile
 constexpr int kKS = 256;      // K of a stage (128 bytes of codes)
-constexpr int kABox = 32;     // rows of one activation box
 
 template <int NT>
 struct Cfg {
@@ -65,8 +59,8 @@ struct Cfg {
   static constexpr int OFF_B = STAGES * A_BYTES;
   static constexpr int OFF_SA = OFF_B + STAGES * B_BYTES;
   static constexpr int OFF_SB = OFF_SA + STAGES * SA_BYTES;
-  static constexpr int OFF_OUT = OFF_SB + STAGES * SB_BYTES;    // a warp: 32 rows x 64 bytes
-  static constexpr int OFF_TILE = OFF_OUT + kEpiWarps * 2048;   // int tile_start[E + 1], off[E + 1]
+  static constexpr int OFF_OUT = OFF_SB + STAGES * SB_BYTES;
+  static constexpr int OFF_TILE = OFF_OUT + kEpiWarps * kStageOut;  // int tile_start[E + 1], off[E + 1]
   static constexpr int OFF_BAR = OFF_TILE + 2 * (kMxMaxExperts + 1) * 4;
   static constexpr int N_BARS = 2 * STAGES + 4 + 2;
   static constexpr int OFF_MISC = OFF_BAR + N_BARS * 8;
@@ -91,31 +85,6 @@ struct Params {
   uint8_t* out_scales;
   int32_t* status;
 };
-
-struct Tile {
-  int e, row0, nrows, n0, nn;
-};
-
-template <int NT>
-__device__ __forceinline__ Tile decode_tile(int t, const int* tile_start, const int* off, int E, int N) {
-  int lo = 0, hi = E;  // largest e with tile_start[e] <= t
-  while (hi - lo > 1) {
-    const int mid = (lo + hi) >> 1;
-    if (tile_start[mid] <= t) lo = mid; else hi = mid;
-  }
-  Tile T;
-  T.e = lo;
-  const int n = off[lo + 1] - off[lo];
-  const int mt = (n + kM - 1) / kM;
-  const int local = t - tile_start[lo];
-  // row tiles inside a weight tile: CTAs that run together share its codes
-  const int nb = local / mt, mb = local - nb * mt;
-  T.row0 = off[lo] + mb * kM;
-  T.nrows = min(kM, n - mb * kM);
-  T.n0 = nb * NT;
-  T.nn = min(NT, N - T.n0);
-  return T;
-}
 
 template <int NT, int OUT>
 __global__ void __launch_bounds__(kThreads, 1) k_mx_gemm(const __grid_constant__ Params P) {
@@ -156,49 +125,20 @@ __global__ void __launch_bounds__(kThreads, 1) k_mx_gemm(const __grid_constant__
   if (warp == 3) tmem_alloc(smem_u32(tmem_slot), C::TMEM_COLS);
   pdl_wait();
   pdl_trigger();
-  // offsets are clamped into [0, rows]: no table can send a tile outside
-  for (int b = tid; b <= E; b += kThreads) {
-    const int v = P.offsets[b];
-    const int c = min(max(v, 0), P.rows);
-    if (c != v || (b == E && v != P.rows)) flag_status(P.status, MOE_DEV_BAD_INDEX);
-    off_s[b] = c;
-  }
-  __syncwarp();
-  __syncthreads();
-  if (warp == 0) {  // tiles per expert -> exclusive scan, a run of experts per lane
-    const int per = (E + 31) / 32, b0 = lane * per;
-    int run = 0;
-    for (int i = 0; i < per; ++i) {
-      const int b = b0 + i;
-      if (b < E) {
-        const int n = max(0, off_s[b + 1] - off_s[b]);
-        tile_start[b] = run;
-        run += (n + kM - 1) / kM * NB;
-      }
-    }
-    int incl = run;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int v = __shfl_up_sync(0xffffffffu, incl, o);
-      if (lane >= o) incl += v;
-    }
-    for (int i = 0; i < per; ++i)
-      if (b0 + i < E) tile_start[b0 + i] += incl - run;
-    if (lane == 31) tile_start[E] = incl;
-  }
+  build_tiles<kM>(P.offsets, E, P.rows, NB, P.status, tile_start, off_s);
   __syncwarp();
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem = *tmem_slot;
-  const int tiles = tile_start[E];
+  const uint32_t tmem = __shfl_sync(0xffffffffu, *tmem_slot, 0);
+  const int tiles = __shfl_sync(0xffffffffu, tile_start[E], 0);
 
   if (warp == 0 || warp == 2) {
     // ---- weights (warp 0), codes of the rows (warp 2) ------------------------
     int s = 0, ph = 0;
     bool ok = true;
     for (int t = blockIdx.x; t < tiles && ok; t += gridDim.x) {
-      const Tile T = decode_tile<NT>(t, tile_start, off_s, E, P.N);
+      const Tile T = decode_tile<kM, NT>(t, tile_start, off_s, E, P.N);
       const int boxes = (T.nrows + kABox - 1) / kABox;
       const bool two_rt = C::RT == 2 && T.nn > 128;
       const uint8_t* sc = P.b_scales + static_cast<size_t>(T.e) * P.mat_stride +
@@ -241,7 +181,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_mx_gemm(const __grid_constant__
     int s = 0, ph = 0;
     bool ok = true;
     for (int t = blockIdx.x; t < tiles && ok; t += gridDim.x) {
-      const Tile T = decode_tile<NT>(t, tile_start, off_s, E, P.N);
+      const Tile T = decode_tile<kM, NT>(t, tile_start, off_s, E, P.N);
       const uint8_t* base = P.a_scales + static_cast<size_t>(T.row0 + lane) * (P.K / 32);
       auto fetch = [&](int kb0, uint4 (&w)[G][2]) {
 #pragma unroll
@@ -292,7 +232,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_mx_gemm(const __grid_constant__
     const uint64_t da0 = desc_sw128(smem_u32(smem)), db0 = desc_sw128(smem_u32(smem + C::OFF_B));
     const uint64_t dsa0 = desc_plain(smem_u32(smem + C::OFF_SA)), dsb0 = desc_plain(smem_u32(smem + C::OFF_SB));
     for (int t = blockIdx.x; t < tiles && ok; t += gridDim.x, ++tile) {
-      const Tile T = decode_tile<NT>(t, tile_start, off_s, E, P.N);
+      const Tile T = decode_tile<kM, NT>(t, tile_start, off_s, E, P.N);
       const uint32_t id0 = idesc_mxf4(T.nn, 0), id1 = idesc_mxf4(T.nn, 1);
       const bool two_rt = C::RT == 2 && T.nn > 128;
       const uint32_t shift = NT == 64 ? (T.n0 >> 5) & 2 : 0;  // second half of a 128-row scale tile
@@ -352,7 +292,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_mx_gemm(const __grid_constant__
     int tile = 0;
     bool ok = true;
     for (int t = blockIdx.x; t < tiles && ok; t += gridDim.x, ++tile) {
-      const Tile T = decode_tile<NT>(t, tile_start, off_s, E, P.N);
+      const Tile T = decode_tile<kM, NT>(t, tile_start, off_s, E, P.N);
       ok = warp_wait(acc_full(tile), (tile >> 1) & 1, abort_flag, P.status);
       if (!ok) break;
       tc_fence_after();
@@ -376,89 +316,9 @@ __global__ void __launch_bounds__(kThreads, 1) k_mx_gemm(const __grid_constant__
         const int grp = last_first && half == 1 ? 4 - i : i;
         const int c = grp * 64;
         if (grp < groups && any) {
-          if (OUT == kMxOutSwiglu) {
-            // 32 gate columns and the 32 up columns of the same features: one 32-block of h
-            uint8_t* hc = static_cast<uint8_t*>(P.out) + static_cast<size_t>(T.row0 + r) * (P.N / 4) + (T.n0 + c) / 4;
-            uint8_t* hs = P.out_scales + static_cast<size_t>(T.row0 + r) * (P.N / 64) + (T.n0 + c) / 64;
-            uint32_t g[32], u[32];
-            tmem_ld32(tb + c, g);
-            tmem_ld32(tb + c + 32, u);
-            tmem_ld_wait();
-            float h[32];
-            uint32_t m = 0;
-#pragma unroll
-            for (int j = 0; j < 32; ++j) {
-              // (a fast division, 2 ulp: the exact one's path for tiny operands, which the rows
-              // past the tile's hold, took 4 times as long as all the rest of the kernel)
-              const float gv = __uint_as_float(g[j]);
-              h[j] = __fdividef(gv, 1.0f + __expf(-gv)) * __uint_as_float(u[j]);
-              m = max(m, __float_as_uint(h[j]) & 0x7FFFFFFFu);
-            }
-            const uint32_t byte = mx_scale_byte(m);
-            uint32_t w[4] = {0, 0, 0, 0};
-            if (byte != 255u) {
-              const float inv = mx_inv_scale(byte);
-#pragma unroll
-              for (int k = 0; k < 4; ++k) {
-                float v[8];
-#pragma unroll
-                for (int j = 0; j < 8; ++j) v[j] = h[8 * k + j] * inv;
-                w[k] = mx_encode8(v);
-              }
-            }
-            if (live) {
-              bad |= byte == 255u;
-              *reinterpret_cast<uint4*>(hc) = make_uint4(w[0], w[1], w[2], w[3]);
-              *hs = static_cast<uint8_t>(byte);
-            }
-          } else {
-            // 64 bytes of every row at a time through the warp's staging rows
-            // (16-byte pieces swizzled by row), so that a store instruction
-            // covers eight whole 64-byte runs
-            constexpr int ES = OUT == kMxOutF32 ? 4 : 2, CW = 64 / ES;
-            uint8_t* st = smem + C::OFF_OUT + (warp - 4) * 2048;
-            uint32_t v[64];
-            tmem_ld32(tb + c, *reinterpret_cast<uint32_t(*)[32]>(v));
-            tmem_ld32(tb + c + 32, *reinterpret_cast<uint32_t(*)[32]>(v + 32));
-            tmem_ld_wait();
-#pragma unroll
-            for (int c1 = 0; c1 < 64; c1 += CW) {
-              __syncwarp();  // the rows staged before have been read
-#pragma unroll
-              for (int j = 0; j < 4; ++j) {
-                uint32_t w[4];
-#pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                  if (OUT == kMxOutF32) {
-                    w[k] = v[c1 + 4 * j + k];
-                  } else {
-                    const float y0 = __uint_as_float(v[c1 + 8 * j + 2 * k]);
-                    const float y1 = __uint_as_float(v[c1 + 8 * j + 2 * k + 1]);
-                    if (OUT == kMxOutF16) {
-                      bad |= !(fabsf(y0) <= 65504.0f) || !(fabsf(y1) <= 65504.0f);
-                      const __half2 h = __floats2half2_rn(y0, y1);
-                      w[k] = *reinterpret_cast<const uint32_t*>(&h);
-                    } else {
-                      const __nv_bfloat162 h = __floats2bfloat162_rn(y0, y1);
-                      w[k] = *reinterpret_cast<const uint32_t*>(&h);
-                    }
-                  }
-                }
-                *reinterpret_cast<uint4*>(st + lane * 64 + ((j ^ ((lane >> 1) & 3)) << 4)) =
-                    make_uint4(w[0], w[1], w[2], w[3]);
-              }
-              __syncwarp();
-              uint8_t* out = static_cast<uint8_t*>(P.out) +
-                             (static_cast<size_t>(T.row0 + 32 * q) * P.N + T.n0 + c + c1) * ES + (lane & 3) * 16;
-#pragma unroll
-              for (int k = 0; k < 4; ++k) {
-                const int row = 8 * k + (lane >> 2);
-                if (32 * q + row < T.nrows)
-                  *reinterpret_cast<uint4*>(out + static_cast<size_t>(row) * P.N * ES) =
-                      *reinterpret_cast<const uint4*>(st + row * 64 + (((lane & 3) ^ ((row >> 1) & 3)) << 4));
-              }
-            }
-          }
+          bad |= store_group<OUT>(
+              P.out, [&](int blk) { return P.out_scales + static_cast<size_t>(T.row0 + r) * (P.N / 64) + blk; }, tb + c,
+              smem + C::OFF_OUT + (warp - 4) * kStageOut, lane, T.row0 + 32 * q, T.nrows - 32 * q, T.n0 + c, P.N);
         }
         if (kShared && i == half && half == (last_first ? 1 : 0)) freed();
       }
@@ -480,29 +340,6 @@ __global__ void __launch_bounds__(kThreads, 1) k_mx_gemm(const __grid_constant__
 }
 
 // ---- host side ----------------------------------------------------------------
-
-PFN_cuTensorMapEncodeTiled_v12000 get_encode() {
-  static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
-  static std::once_flag once;
-  std::call_once(once, [] {
-    void* p = nullptr;
-    cudaDriverEntryPointQueryResult q;
-    if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &p, cudaEnableDefault, &q) == cudaSuccess &&
-        q == cudaDriverEntryPointSuccess)
-      fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(p);
-  });
-  return fn;
-}
-
-bool encode_bytes(CUtensorMap* m, int rank, const void* base, const cuuint64_t* dims, const cuuint64_t* strides,
-                  const cuuint32_t* box) {
-  auto fn = get_encode();
-  if (!fn) return false;
-  const cuuint32_t es[3] = {1, 1, 1};
-  return fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, rank, const_cast<void*>(base), dims, strides, box, es,
-            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
 
 template <int NT, int OUT>
 moe_status_t launch(const MxGemmArgs& a, cudaStream_t s) {
@@ -563,6 +400,7 @@ template <int OUT>
 moe_status_t launch_out(const MxGemmArgs& a, cudaStream_t s) {
   // Widest weight tile that still gives every SM one: wide tiles read the
   // rows fewer times, narrow ones spread a small call's weights over more SMs.
+  if (a.paired) return launch_mx_pair(a, s);
   const long mt = std::max<long>(std::min(a.E, a.rows), a.rows / kM);
   if (mt * (a.N / 256) >= 148) return launch<256, OUT>(a, s);
   if (mt * (a.N / 128) >= 148) return launch<128, OUT>(a, s);
@@ -615,6 +453,14 @@ moe_status_t check(const char* fn, const void* codes, const void* scales, const 
 
 size_t up256(size_t n) { return (n + 255) / 256 * 256; }
 
+// Two SMs to a tile of 256 rows: where experts have that many rows on average
+// and every pair of SMs gets a tile (fewer rows would leave half of the pair's
+// products unused).
+constexpr int kPairRows = 192;
+bool paired(int rows, int E, int N) {
+  return rows > 0 && rows / std::min(E, rows) >= kPairRows && static_cast<long>(rows) / 256 * (N / 256) >= 74;
+}
+
 }  // namespace
 }  // namespace moeq
 
@@ -622,13 +468,29 @@ using namespace moeq;
 
 extern "C" {
 
+size_t moe_mx_gemm_workspace_bytes(int rows, int E, int N, int K) {
+  if (rows <= 0 || E <= 0 || N <= 0 || K <= 0 || !paired(rows, E, N)) return 0;
+  return mx_tiled_bytes(rows, E, K);
+}
+
 moe_status_t moe_mx_grouped_gemm(const void* codes, const void* scales, const int32_t* offsets, const void* mats,
-                                 int rows, int E, int N, int K, int out_dtype, void* out, int32_t* status,
-                                 moe_stream_t stream) {
-  const moe_status_t st = check("moe_mx_grouped_gemm", codes, scales, offsets, mats, out, rows, E, N, K);
+                                 int rows, int E, int N, int K, int out_dtype, void* out, void* workspace,
+                                 size_t workspace_bytes, int32_t* status, moe_stream_t stream) {
+  const char* fn = "moe_mx_grouped_gemm";
+  moe_status_t st = check(fn, codes, scales, offsets, mats, out, rows, E, N, K);
   if (st != MOE_OK) return st;
   if (out_dtype != MOE_F32 && out_dtype != MOE_BF16 && out_dtype != MOE_F16) {
-    set_error("moe_mx_grouped_gemm: unknown output dtype %d", out_dtype);
+    set_error("%s: unknown output dtype %d", fn, out_dtype);
+    return MOE_ERR_INVALID_ARG;
+  }
+  if (rows == 0) return MOE_OK;
+  const size_t need = moe_mx_gemm_workspace_bytes(rows, E, N, K);
+  if (need && (!workspace || workspace_bytes < need)) {
+    set_error("%s: workspace %zu < %zu bytes", fn, workspace_bytes, need);
+    return MOE_ERR_WORKSPACE;
+  }
+  if (need && !aligned16(workspace)) {
+    set_error("%s: workspace must be 16-byte aligned", fn);
     return MOE_ERR_INVALID_ARG;
   }
   MxGemmArgs a{};
@@ -644,12 +506,23 @@ moe_status_t moe_mx_grouped_gemm(const void* codes, const void* scales, const in
   a.out_kind = out_dtype == MOE_F32 ? kMxOutF32 : out_dtype == MOE_BF16 ? kMxOutBf16 : kMxOutF16;
   a.out = out;
   a.status = status;
+  a.paired = need != 0;
+  if (a.paired) {
+    st = launch_mx_tile_scales(a.a_scales, offsets, rows, E, K, static_cast<uint8_t*>(workspace),
+                               static_cast<cudaStream_t>(stream));
+    if (st != MOE_OK) return st;
+    a.a_tiles = static_cast<const uint8_t*>(workspace);
+  }
   return launch_mx_gemm(a, static_cast<cudaStream_t>(stream));
 }
 
-size_t moe_ffn_mx_workspace_bytes(int rows, int F) {
-  if (rows <= 0 || F <= 0) return 256;
-  return up256(static_cast<size_t>(rows) * (F / 2)) + up256(static_cast<size_t>(rows) * (F / 32));
+// Codes of h, its scales, and (two SMs to a tile) the rows' scales in tiles.
+size_t moe_ffn_mx_workspace_bytes(int rows, int E, int d, int F) {
+  if (rows <= 0 || E <= 0 || d <= 0 || F <= 0) return 256;
+  const size_t hc = up256(static_cast<size_t>(rows) * (F / 2));
+  const size_t flat = up256(static_cast<size_t>(rows) * (F / 32));
+  if (!paired(rows, E, 2 * F) || !paired(rows, E, d)) return hc + flat;
+  return hc + std::max(flat, up256(mx_tiled_bytes(rows, E, F))) + mx_tiled_bytes(rows, E, d);
 }
 
 moe_status_t moe_grouped_ffn_mx(const void* codes, const void* scales, const int32_t* offsets, const void* blobs,
@@ -660,8 +533,9 @@ moe_status_t moe_grouped_ffn_mx(const void* codes, const void* scales, const int
   if (st == MOE_OK) st = check(fn, codes, scales, offsets, blobs, y_perm, rows, E, 2 * F, d);
   if (st != MOE_OK) return st;
   if (rows == 0) return MOE_OK;
-  if (!workspace || workspace_bytes < moe_ffn_mx_workspace_bytes(rows, F)) {
-    set_error("%s: workspace %zu < %zu bytes", fn, workspace_bytes, moe_ffn_mx_workspace_bytes(rows, F));
+  const size_t need = moe_ffn_mx_workspace_bytes(rows, E, d, F);
+  if (!workspace || workspace_bytes < need) {
+    set_error("%s: workspace %zu < %zu bytes", fn, workspace_bytes, need);
     return MOE_ERR_WORKSPACE;
   }
   if (!aligned16(workspace)) {
@@ -684,10 +558,18 @@ moe_status_t moe_grouped_ffn_mx(const void* codes, const void* scales, const int
   a.out = hc;
   a.out_scales = hs;
   a.status = status;
+  a.paired = paired(rows, E, 2 * F) && paired(rows, E, d);
+  if (a.paired) {
+    uint8_t* xs = static_cast<uint8_t*>(workspace) + need - mx_tiled_bytes(rows, E, d);
+    st = launch_mx_tile_scales(a.a_scales, offsets, rows, E, d, xs, static_cast<cudaStream_t>(stream));
+    if (st != MOE_OK) return st;
+    a.a_tiles = xs;
+  }
   st = launch_mx_gemm(a, static_cast<cudaStream_t>(stream));
   if (st != MOE_OK) return st;
   a.a_codes = hc;
   a.a_scales = hs;
+  a.a_tiles = hs;
   a.mats = static_cast<const uint8_t*>(blobs) + mx_matrix_bytes(2 * F, d);
   a.N = d;
   a.K = F;
