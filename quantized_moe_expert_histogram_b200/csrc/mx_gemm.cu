@@ -34,6 +34,7 @@
 // Every wait is bounded; on a timeout the CTA raises MOE_DEV_TIMEOUT, lets its
 // copies land, frees tensor memory and returns.
 #include <atomic>
+#include <type_traits>
 
 #include "mx_gemm.cuh"
 
@@ -171,7 +172,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_mx_gemm(const __grid_constant__
       const uint64_t t0 = global_ns();
       for (int i = 0; i < C::STAGES; ++i) {
         const int p = i < s ? ph : ph ^ 1;
-        while (!mbar_try(full(i), p, 1000u) && global_ns() - t0 < kWaitLimitNs) {}
+        while (!mbar_try(full(i), p) && global_ns() - t0 < kWaitLimitNs) {}
       }
       __syncwarp();
     }
@@ -244,45 +245,49 @@ __global__ void __launch_bounds__(kThreads, 1) k_mx_gemm(const __grid_constant__
       }
       tc_fence_after();
       const uint32_t d = tmem + (tile & 1) * C::ACC1;
-      for (int kb = 0; kb < KB; ++kb, ++n) {
-        ok = warp_wait(full(s), ph, abort_flag, P.status);
-        if (!ok) break;
-        if (C::SETS < C::STAGES && n >= C::SETS) {
-          // the products of SETS stages ago, which read this set of scale columns
-          const int so = (n - C::SETS) % C::STAGES, po = ((n - C::SETS) / C::STAGES) & 1;
-          ok = warp_wait(empty(so), po, abort_flag, P.status);
-          if (!ok) break;
-        }
+      // A stage's copies and products in one straight line: between branches the
+      // compiler moved every operand through ordinary registers (60 cycles an
+      // instruction instead of 10).
+      auto stage = [&](auto two, uint32_t later) {
+        if (!warp_wait(full(s), ph, abort_flag, P.status)) return false;
+        // the products of SETS stages ago, which read this set of scale columns
+        if (C::SETS < C::STAGES && n >= C::SETS &&
+            !warp_wait(empty((n - C::SETS) % C::STAGES), ((n - C::SETS) / C::STAGES) & 1, abort_flag, P.status))
+          return false;
         tc_fence_after();
         const uint32_t sfa = tmem + C::SF0 + (C::SETS < C::STAGES ? n % C::SETS : s) * C::SF_COLS, sfb = sfa + 8;
         const uint64_t da = da0 + s * (C::A_BYTES >> 4), db = db0 + s * (C::B_BYTES >> 4);
         const uint64_t dsa = dsa0 + s * (C::SA_BYTES >> 4), dsb = dsb0 + s * (C::SB_BYTES >> 4);
-        const bool two = P.K - kb * kKS > 128;
+        // (a tile of 128 of 256 outputs: the second tile of scales is stale and unused)
         tc_copy_scales(sfa, dsa);
         tc_copy_scales(sfb, dsb);
-        if (two_rt) tc_copy_scales(sfb + 4, dsb + 64);
-        if (two) {
+        if constexpr (C::RT == 2) tc_copy_scales(sfb + 4, dsb + 64);
+        if constexpr (two.value) {
           tc_copy_scales(sfa + 4, dsa + 32);
           tc_copy_scales(sfb + 4 * C::RT, dsb + 32);
-          if (two_rt) tc_copy_scales(sfb + 4 * C::RT + 4, dsb + 96);
+          if constexpr (C::RT == 2) tc_copy_scales(sfb + 4 * C::RT + 4, dsb + 96);
         }
         const uint32_t fb = sfb + shift;
-        mma_mxf4(d, da, db, id0, sfa, fb, kb != 0);
+        mma_mxf4(d, da, db, id0, sfa, fb, later);
         mma_mxf4(d, da + 2, db + 2, id1, sfa, fb, 1u);
-        if (two) {
+        if constexpr (two.value) {
           mma_mxf4(d, da + 4, db + 4, id0, sfa + 4, fb + 4 * C::RT, 1u);
           mma_mxf4(d, da + 6, db + 6, id1, sfa + 4, fb + 4 * C::RT, 1u);
         }
         tc_commit(empty(s));
         if (++s == C::STAGES) { s = 0; ph ^= 1; }
-      }
+        ++n;
+        return true;
+      };
+      for (int kb = 0; kb < P.K / kKS && ok; ++kb) ok = stage(std::true_type{}, kb != 0);
+      if (ok && P.K % kKS) ok = stage(std::false_type{}, P.K > kKS);
       if (!ok) break;
       tc_commit(acc_full(tile));
     }
     // every product issued here completes before tensor memory is released
     tc_commit(drain_bar);
     const uint64_t t0 = global_ns();
-    while (!mbar_try(drain_bar, 0, 1000u) && global_ns() - t0 < kWaitLimitNs) {}
+    while (!mbar_try(drain_bar, 0) && global_ns() - t0 < kWaitLimitNs) {}
     __syncwarp();
   } else if (warp >= 4) {
     // ---- epilogue: lane = row of the tile, quadrant = warp % 4; the quadrant's
@@ -332,7 +337,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_mx_gemm(const __grid_constant__
   if (lane == 0) mbar_arrive(exit_bar);
   if (warp == 3) {  // frees tensor memory once every warp has left its loop
     const uint64_t t0 = global_ns();
-    while (!mbar_try(exit_bar, 0, 1000u) && global_ns() - t0 < 2 * kWaitLimitNs) {}
+    while (!mbar_try(exit_bar, 0) && global_ns() - t0 < 2 * kWaitLimitNs) {}
     __syncwarp();
     tc_fence_after();
     tmem_free(tmem, C::TMEM_COLS);

@@ -20,6 +20,7 @@
 // epilogue that forms them.  Nothing touches the other CTA after the cluster
 // barrier that ends the kernel.
 #include <atomic>
+#include <type_traits>
 
 #include "mx_gemm.cuh"
 
@@ -120,18 +121,19 @@ __device__ __forceinline__ void arrive_at(uint32_t cluster_bar) {
 // Bounded wait by a whole warp for arrivals from either CTA.
 __device__ __forceinline__ bool warp_wait_cluster(uint32_t bar, uint32_t parity, volatile int* abort_flag,
                                                   int32_t* status) {
-  auto attempt = [&] {
+  auto attempt = [&]() -> bool {
     uint32_t ok;
     asm volatile(
         "{\n\t.reg .pred P;\n\t"
-        "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 P, [%1], %2, %3;\n\t"
+        "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 P, [%1], %2;\n\t"
         "selp.b32 %0, 1, 0, P;\n\t}"
         : "=r"(ok)
-        : "r"(bar), "r"(parity), "r"(20000u)
+        : "r"(bar), "r"(parity)
         : "memory");
     return ok != 0;
   };
   bool ok = attempt();
+  if (__all_sync(0xffffffffu, ok)) return true;
   uint64_t t0 = 0;
   for (uint32_t i = 1; !ok; ++i) {
     ok = attempt();
@@ -289,7 +291,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_mx_pair(const __grid_constant__
       const uint64_t t0 = global_ns();
       for (int i = 0; i < kStages; ++i) {
         const int p = i < s ? ph : ph ^ 1;
-        while (!mbar_try(full(i), p, 1000u) && global_ns() - t0 < kWaitLimitNs) {}
+        while (!mbar_try(full(i), p) && global_ns() - t0 < kWaitLimitNs) {}
       }
       __syncwarp();
     }
@@ -304,50 +306,51 @@ __global__ void __launch_bounds__(kThreads, 1) k_mx_pair(const __grid_constant__
         const Tile T = decode_tile<kM, kNT>(t, tile_start, off_s, E, P.N);
         // M = 256 across the pair
         const uint32_t id0 = idesc_mxf4(T.nn, 0) + (8u << 24), id1 = idesc_mxf4(T.nn, 1) + (8u << 24);
-        const bool two_rt = T.nn > 128;
         if (tile >= 1) {
           ok = warp_wait_cluster(acc_free(tile - 1), ((tile - 1) >> 1) & 1, abort_flag, P.status);
           if (!ok) break;
         }
         tc_fence_after();
         const uint32_t d = tmem + (tile & 1) * kAcc1;
-        for (int kb = 0; kb < KB; ++kb, ++n) {
-          ok = warp_wait_cluster(full(s), ph, abort_flag, P.status);
-          if (!ok) break;
-          if (n >= kSets) {
-            // the products of kSets stages ago, which read this set of scale columns
-            ok = warp_wait(empty((n - kSets) % kStages), ((n - kSets) / kStages) & 1, abort_flag, P.status);
-            if (!ok) break;
-          }
+        // (a stage's copies and products in one straight line, as in mx_gemm.cu)
+        auto stage = [&](auto two, uint32_t later) {
+          if (!warp_wait_cluster(full(s), ph, abort_flag, P.status)) return false;
+          // the products of kSets stages ago, which read this set of scale columns
+          if (n >= kSets && !warp_wait(empty((n - kSets) % kStages), ((n - kSets) / kStages) & 1, abort_flag, P.status))
+            return false;
           tc_fence_after();
           const uint32_t sfa = tmem + kSF0 + (n % kSets) * kSFCols, sfb = sfa + 8;
           const uint64_t da = da0 + s * (kA >> 4), db = db0 + s * (kB >> 4);
           const uint64_t dsa = dsa0 + s * (kSA >> 4), dsb = dsb0 + s * (kSB >> 4);
-          const bool two = P.K - kb * kKS > 128;
+          // (a tile of 128 of 256 outputs: the second tile of scales is stale and unused)
           pair_copy_scales(sfa, dsa);
           pair_copy_scales(sfb, dsb);
-          if (two_rt) pair_copy_scales(sfb + 4, dsb + 64);
-          if (two) {
+          pair_copy_scales(sfb + 4, dsb + 64);
+          if constexpr (two.value) {
             pair_copy_scales(sfa + 4, dsa + 32);
             pair_copy_scales(sfb + 8, dsb + 32);
-            if (two_rt) pair_copy_scales(sfb + 12, dsb + 96);
+            pair_copy_scales(sfb + 12, dsb + 96);
           }
-          pair_mma(d, da, db, id0, sfa, sfb, kb != 0);
+          pair_mma(d, da, db, id0, sfa, sfb, later);
           pair_mma(d, da + 2, db + 2, id1, sfa, sfb, 1u);
-          if (two) {
+          if constexpr (two.value) {
             pair_mma(d, da + 4, db + 4, id0, sfa + 4, sfb + 8, 1u);
             pair_mma(d, da + 6, db + 6, id1, sfa + 4, sfb + 8, 1u);
           }
           pair_commit(empty(s));
           if (++s == kStages) { s = 0; ph ^= 1; }
-        }
+          ++n;
+          return true;
+        };
+        for (int kb = 0; kb < P.K / kKS && ok; ++kb) ok = stage(std::true_type{}, kb != 0);
+        if (ok && P.K % kKS) ok = stage(std::false_type{}, P.K > kKS);
         if (!ok) break;
         pair_commit(acc_full(tile));
       }
       // every product completes before the cluster goes
       pair_commit(drain_bar);
       const uint64_t t0 = global_ns();
-      while (!mbar_try(drain_bar, 0, 1000u) && global_ns() - t0 < kWaitLimitNs) {}
+      while (!mbar_try(drain_bar, 0) && global_ns() - t0 < kWaitLimitNs) {}
       __syncwarp();
     }
   } else if (warp >= 4) {

@@ -22,16 +22,16 @@ __device__ __forceinline__ void mbar_init_fence() {
 __device__ __forceinline__ void mbar_arrive(uint32_t bar) {
   asm volatile("mbarrier.arrive.release.cta.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
 }
-// Lets the hardware suspend the thread for up to hint_ns while the phase is
-// incomplete.
-__device__ __forceinline__ bool mbar_try(uint32_t bar, uint32_t parity, uint32_t hint_ns = 0) {
+// Lets the hardware suspend the thread for a while when the phase is
+// incomplete (its own limit: 3 % less time than with a longer one asked for).
+__device__ __forceinline__ bool mbar_try(uint32_t bar, uint32_t parity) {
   uint32_t ok;
   asm volatile(
       "{\n\t.reg .pred P;\n\t"
-      "mbarrier.try_wait.parity.shared::cta.b64 P, [%1], %2, %3;\n\t"
+      "mbarrier.try_wait.parity.shared::cta.b64 P, [%1], %2;\n\t"
       "selp.b32 %0, 1, 0, P;\n\t}"
       : "=r"(ok)
-      : "r"(bar), "r"(parity), "r"(hint_ns)
+      : "r"(bar), "r"(parity)
       : "memory");
   return ok != 0;
 }
@@ -49,7 +49,7 @@ __device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, volatil
                                           uint64_t limit_ns = kWaitLimitNs) {
   uint64_t t0 = 0;
   for (uint32_t i = 1;; ++i) {
-    if (mbar_try(bar, parity, 20000u)) return true;
+    if (mbar_try(bar, parity)) return true;
     if ((i & 7) == 0) {
       // the timer is read only here: read at the start of a wait, it cost more
       // than the wait (stages of 1000 to 2300 cycles)
@@ -67,6 +67,7 @@ __device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, volatil
 // The same by a whole warp, which reconverges and agrees on the outcome.
 __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, volatile int* abort_flag, int32_t* status,
                                           uint64_t limit_ns = kWaitLimitNs) {
+  if (__all_sync(0xffffffffu, mbar_try(bar, parity))) return true;
   const bool ok = mbar_wait(bar, parity, abort_flag, status, limit_ns);
   __syncwarp();
   return __all_sync(0xffffffffu, ok);

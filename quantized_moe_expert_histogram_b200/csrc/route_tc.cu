@@ -167,7 +167,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_route_tc(const __grid_constant_
     if (!ok) {  // the copies in flight land before the CTA goes
       const uint64_t g0 = global_ns();
       for (int c = max(0, armed - kStages); c < armed; ++c)
-        while (!mbar_try(full(c % kStages), (c / kStages) & 1, 1000u) && global_ns() - g0 < kWaitLimitNs) {}
+        while (!mbar_try(full(c % kStages), (c / kStages) & 1) && global_ns() - g0 < kWaitLimitNs) {}
       __syncwarp();
     }
   } else if (warp == 1) {
@@ -193,7 +193,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_route_tc(const __grid_constant_
     if (ok) tc_commit(ml_full);
     tc_commit(drain_bar);  // every product completes before tensor memory is released
     const uint64_t g0 = global_ns();
-    while (!mbar_try(drain_bar, 0, 1000u) && global_ns() - g0 < kWaitLimitNs) {}
+    while (!mbar_try(drain_bar, 0) && global_ns() - g0 < kWaitLimitNs) {}
     __syncwarp();
   } else if (warp >= 4) {
     // lane = expert 32 q + lane of the tile, 128 tokens; as a norm thread, token `row`
@@ -266,7 +266,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_route_tc(const __grid_constant_
   if (lane == 0) mbar_arrive(exit_bar);
   if (warp == 2) {  // frees tensor memory once every warp has left its loop
     const uint64_t g0 = global_ns();
-    while (!mbar_try(exit_bar, 0, 1000u) && global_ns() - g0 < 2 * kWaitLimitNs) {}
+    while (!mbar_try(exit_bar, 0) && global_ns() - g0 < 2 * kWaitLimitNs) {}
     __syncwarp();
     tc_fence_after();
     tmem_free(tmem, 512);
