@@ -435,15 +435,10 @@ MOE_API moe_status_t moe_mx_pack_ffn(const void* w_gate, const void* w_up, const
  * no expert keep what they held.  An fp16 output beyond the range flags
  * MOE_DEV_RANGE, offsets outside [0, rows] are clamped and flag
  * MOE_DEV_BAD_INDEX.  Requires N, K multiples of 128, E <= 256 and 16-byte
- * aligned codes, scales, mats and out.
- *   workspace      >= moe_mx_gemm_workspace_bytes(rows, E, N, K) bytes (enough
- *                  for fewer rows too), 16-byte aligned; NULL where that is 0
- *                  (smaller batches) */
+ * aligned codes, scales, mats and out. */
 MOE_API moe_status_t moe_mx_grouped_gemm(const void* codes, const void* scales, const int32_t* offsets,
                                          const void* mats, int rows, int E, int N, int K, int out_dtype, void* out,
-                                         void* workspace, size_t workspace_bytes, int32_t* status,
-                                         moe_stream_t stream);
-MOE_API size_t moe_mx_gemm_workspace_bytes(int rows, int E, int N, int K);
+                                         int32_t* status, moe_stream_t stream);
 
 /* moe_grouped_ffn_mx -- the grouped expert FFN on MXFP4 rows and blobs, the
  * MXFP4 counterpart of moe_grouped_ffn_wq:
@@ -451,8 +446,8 @@ MOE_API size_t moe_mx_gemm_workspace_bytes(int rows, int E, int N, int K);
  *     y_perm[p] = Wd_e hq[p],  hq[p] = MXFP4 of h[p]
  *   codes, scales  rows of d (moe_mx_quantize); offsets int32 [E + 1]; blobs
  *                  E FFN blobs (moe_mx_pack_ffn)
- *   workspace      >= moe_ffn_mx_workspace_bytes(rows, E, d, F) bytes (hq, and
- *                  scales; enough for fewer rows too), 16-byte aligned
+ *   workspace      >= moe_ffn_mx_workspace_bytes(rows, F) bytes (hq), 16-byte
+ *                  aligned
  *   y_perm         fp16 [rows][d], for moe_unpermute_combine
  * Sums are fp32, y_perm rounded once; range, offsets and requirements as in
  * moe_mx_grouped_gemm (a block of h with an Inf or a NaN flags MOE_DEV_RANGE
@@ -460,7 +455,7 @@ MOE_API size_t moe_mx_gemm_workspace_bytes(int rows, int E, int N, int K);
 MOE_API moe_status_t moe_grouped_ffn_mx(const void* codes, const void* scales, const int32_t* offsets,
                                         const void* blobs, int rows, int E, int d, int F, void* workspace,
                                         size_t workspace_bytes, void* y_perm, int32_t* status, moe_stream_t stream);
-MOE_API size_t moe_ffn_mx_workspace_bytes(int rows, int E, int d, int F);
+MOE_API size_t moe_ffn_mx_workspace_bytes(int rows, int F);
 
 /* ---------------------------------------------------------------------
  * Offload mode ([ExactMoE] compressed experts in host memory, GPU slot

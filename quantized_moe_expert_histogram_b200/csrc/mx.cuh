@@ -91,23 +91,11 @@ struct MxGemmArgs {
   int rows, E, N, K;
   int out_kind;  // kMxOut*
   void* out;     // [rows][N]; kMxOutSwiglu: codes [rows][N/4] of h [rows][N/2]
-  uint8_t* out_scales;  // kMxOutSwiglu: [rows][N/64], or (paired) tiles as row_tiles
-  // paired: two SMs to a tile; the rows' scales in tiles as the weights' are,
-  // an expert's rows starting a new tile (launch_mx_tile_scales)
-  const uint8_t* a_tiles;
-  bool paired;
+  uint8_t* out_scales;  // kMxOutSwiglu: [rows][N/64]
   int32_t* status;
 };
 enum { kMxOutF16 = 0, kMxOutBf16 = 1, kMxOutF32 = 2, kMxOutSwiglu = 3 };
 moe_status_t launch_mx_gemm(const MxGemmArgs& a, cudaStream_t s);
-moe_status_t launch_mx_pair(const MxGemmArgs& a, cudaStream_t s);
-
-// Scale tiles (128 rows x 128 K, 512 bytes) of rows in experts' order: at most
-// rows / 128 + E row tiles.
-inline size_t mx_row_tiles(int rows, int E) { return static_cast<size_t>(rows) / 128 + std::min(E, rows); }
-inline size_t mx_tiled_bytes(int rows, int E, int K) { return mx_row_tiles(rows, E) * (K / 128) * 512; }
-moe_status_t launch_mx_tile_scales(const uint8_t* scales, const int32_t* offsets, int rows, int E, int K,
-                                   uint8_t* tiles, cudaStream_t s);
 constexpr int kMxMaxExperts = 256;
 
 }  // namespace moeq

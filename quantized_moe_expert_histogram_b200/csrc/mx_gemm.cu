@@ -33,10 +33,14 @@
 //
 // Every wait is bounded; on a timeout the CTA raises MOE_DEV_TIMEOUT, lets its
 // copies land, frees tensor memory and returns.
+#include <cudaTypedefs.h>
+
 #include <atomic>
+#include <mutex>
 #include <type_traits>
 
-#include "mx_gemm.cuh"
+#include "mx.cuh"
+#include "ptx.cuh"
 
 namespace moeq {
 namespace {
@@ -46,6 +50,9 @@ using namespace ptx;
 constexpr int kThreads = 384;
 constexpr int kM = 128;       // rows of a tile
 constexpr int kKS = 256;      // K of a stage (128 bytes of codes)
+constexpr int kABox = 32;     // rows of one activation box
+constexpr int kEpiWarps = 8;
+constexpr int kStageOut = 1024;  // staging bytes of an epilogue warp: 32 rows x 32 bytes
 
 template <int NT>
 struct Cfg {
@@ -87,6 +94,161 @@ struct Params {
   int32_t* status;
 };
 
+struct Tile {
+  int e, row0, nrows, n0, nn;
+};
+
+template <int NT>
+__device__ __forceinline__ Tile decode_tile(int t, const int* tile_start, const int* off, int E, int N) {
+  int lo = 0, hi = E;  // largest e with tile_start[e] <= t
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (tile_start[mid] <= t) lo = mid; else hi = mid;
+  }
+  const int o0 = off[lo], o1 = off[lo + 1], start = tile_start[lo];
+  Tile T;
+  T.e = lo;
+  const int n = o1 - o0;
+  const int mt = (n + kM - 1) / kM;
+  const int local = t - start;
+  // row tiles inside a weight tile: CTAs that run together share its codes
+  const int nb = local / mt, mb = local - nb * mt;
+  T.row0 = o0 + mb * kM;
+  T.nrows = min(kM, n - mb * kM);
+  T.n0 = nb * NT;
+  T.nn = min(NT, N - T.n0);
+  return T;
+}
+
+
+// Tiles of 128 rows per expert -> exclusive scan over the experts, by all
+// threads; ends with warp 0 having written tile_start (the caller
+// synchronises).  Offsets are clamped into [0, rows]: no table can send a tile
+// outside.
+__device__ __forceinline__ void build_tiles(const int32_t* offsets, int E, int rows, int NB, int32_t* status,
+                                            int* tile_start, int* off_s) {
+  const int tid = threadIdx.x, lane = tid & 31;
+  for (int b = tid; b <= E; b += blockDim.x) {
+    const int v = offsets[b];
+    const int c = min(max(v, 0), rows);
+    if (c != v || (b == E ? v != rows : offsets[b + 1] < v)) flag_status(status, MOE_DEV_BAD_INDEX);
+    off_s[b] = c;
+  }
+  __syncwarp();
+  __syncthreads();
+  if (tid < 32) {  // a run of experts per lane
+    const int per = (E + 31) / 32, b0 = lane * per;
+    int run = 0;
+    for (int i = 0; i < per; ++i) {
+      const int b = b0 + i;
+      if (b < E) {
+        const int n = max(0, off_s[b + 1] - off_s[b]);
+        tile_start[b] = run;
+        run += (n + kM - 1) / kM * NB;
+      }
+    }
+    int incl = run;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int v = __shfl_up_sync(0xffffffffu, incl, o);
+      if (lane >= o) incl += v;
+    }
+    for (int i = 0; i < per; ++i)
+      if (b0 + i < E) tile_start[b0 + i] += incl - run;
+    if (lane == 31) tile_start[E] = incl;
+  }
+}
+
+// 64 columns (outputs n0 .. n0 + 63) of a warp's 32 rows (row0 .., the first
+// `live` of them exist) from tensor memory at taddr to the output; whether a
+// value left the range.
+template <int OUT>
+__device__ __forceinline__ bool store_group(void* out_v, uint8_t* out_scales, uint32_t taddr, uint8_t* st, int lane, int row0,
+                                            int live, int n0, int N) {
+  bool bad = false;
+  if (OUT == kMxOutSwiglu) {
+    // 32 gate columns and the 32 up columns of the same features: one 32-block of h
+    uint32_t g[32], u[32];
+    tmem_ld32(taddr, g);
+    tmem_ld32(taddr + 32, u);
+    tmem_ld_wait();
+    float h[32];
+    uint32_t m = 0;
+#pragma unroll
+    for (int j = 0; j < 32; ++j) {
+      // (a fast division, 2 ulp: the exact one's path for tiny operands, which the rows
+      // past the tile's hold, took 4 times as long as all the rest of the kernel)
+      const float gv = __uint_as_float(g[j]);
+      h[j] = __fdividef(gv, 1.0f + __expf(-gv)) * __uint_as_float(u[j]);
+      m = max(m, __float_as_uint(h[j]) & 0x7FFFFFFFu);
+    }
+    const uint32_t byte = mx_scale_byte(m);
+    uint32_t w[4] = {0, 0, 0, 0};
+    if (byte != 255u) {
+      const float inv = mx_inv_scale(byte);
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        float v[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[j] = h[8 * k + j] * inv;
+        w[k] = mx_encode8(v);
+      }
+    }
+    if (lane < live) {
+      bad = byte == 255u;
+      const size_t row = static_cast<size_t>(row0 + lane);
+      *reinterpret_cast<uint4*>(static_cast<uint8_t*>(out_v) + row * (N / 4) + n0 / 4) =
+          make_uint4(w[0], w[1], w[2], w[3]);
+      out_scales[row * (N / 64) + n0 / 64] = static_cast<uint8_t>(byte);
+    }
+    return bad;
+  }
+  // 32 bytes of every row at a time through the warp's staging rows (16-byte
+  // pieces swapped by row), so that a store instruction covers whole sectors
+  constexpr int ES = OUT == kMxOutF32 ? 4 : 2, CW = 32 / ES;
+  uint8_t* out = static_cast<uint8_t*>(out_v) + (static_cast<size_t>(row0) * N + n0) * ES + (lane & 1) * 16;
+  uint32_t v[32];
+#pragma unroll
+  for (int c = 0; c < 64; c += CW) {
+    if (c % 32 == 0) {
+      tmem_ld32(taddr + c, v);
+      tmem_ld_wait();
+    }
+    __syncwarp();  // the rows staged before have been read
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      uint32_t w[4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        if (OUT == kMxOutF32) {
+          w[k] = v[c % 32 + 4 * j + k];
+        } else {
+          const float y0 = __uint_as_float(v[c % 32 + 8 * j + 2 * k]);
+          const float y1 = __uint_as_float(v[c % 32 + 8 * j + 2 * k + 1]);
+          if (OUT == kMxOutF16) {
+            bad |= !(fabsf(y0) <= 65504.0f) || !(fabsf(y1) <= 65504.0f);
+            const __half2 h = __floats2half2_rn(y0, y1);
+            w[k] = *reinterpret_cast<const uint32_t*>(&h);
+          } else {
+            const __nv_bfloat162 h = __floats2bfloat162_rn(y0, y1);
+            w[k] = *reinterpret_cast<const uint32_t*>(&h);
+          }
+        }
+      }
+      *reinterpret_cast<uint4*>(st + lane * 32 + ((j ^ ((lane >> 2) & 1)) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
+    }
+    __syncwarp();
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      const int row = 16 * k + (lane >> 1);
+      if (row < live)
+        *reinterpret_cast<uint4*>(out + (static_cast<size_t>(row) * N + c) * ES) =
+            *reinterpret_cast<const uint4*>(st + row * 32 + (((lane & 1) ^ ((row >> 2) & 1)) << 4));
+    }
+  }
+  return bad && lane < live;
+}
+
 template <int NT, int OUT>
 __global__ void __launch_bounds__(kThreads, 1) k_mx_gemm(const __grid_constant__ Params P) {
   using C = Cfg<NT>;
@@ -105,7 +267,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_mx_gemm(const __grid_constant__
   const uint32_t drain_bar = bar0 + 8u * (2 * C::STAGES + 4);
   const uint32_t exit_bar = drain_bar + 8u;
 
-  const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int E = P.E, NB = (P.N + NT - 1) / NT;
   const int KB = (P.K + kKS - 1) / kKS;  // stages of a tile; the last may hold 128 K
 
@@ -126,20 +288,20 @@ __global__ void __launch_bounds__(kThreads, 1) k_mx_gemm(const __grid_constant__
   if (warp == 3) tmem_alloc(smem_u32(tmem_slot), C::TMEM_COLS);
   pdl_wait();
   pdl_trigger();
-  build_tiles<kM>(P.offsets, E, P.rows, NB, P.status, tile_start, off_s);
+  build_tiles(P.offsets, E, P.rows, NB, P.status, tile_start, off_s);
   __syncwarp();
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem = __shfl_sync(0xffffffffu, *tmem_slot, 0);
-  const int tiles = __shfl_sync(0xffffffffu, tile_start[E], 0);
+  const uint32_t tmem = *tmem_slot;
+  const int tiles = tile_start[E];
 
   if (warp == 0 || warp == 2) {
     // ---- weights (warp 0), codes of the rows (warp 2) ------------------------
     int s = 0, ph = 0;
     bool ok = true;
     for (int t = blockIdx.x; t < tiles && ok; t += gridDim.x) {
-      const Tile T = decode_tile<kM, NT>(t, tile_start, off_s, E, P.N);
+      const Tile T = decode_tile<NT>(t, tile_start, off_s, E, P.N);
       const int boxes = (T.nrows + kABox - 1) / kABox;
       const bool two_rt = C::RT == 2 && T.nn > 128;
       const uint8_t* sc = P.b_scales + static_cast<size_t>(T.e) * P.mat_stride +
@@ -182,7 +344,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_mx_gemm(const __grid_constant__
     int s = 0, ph = 0;
     bool ok = true;
     for (int t = blockIdx.x; t < tiles && ok; t += gridDim.x) {
-      const Tile T = decode_tile<kM, NT>(t, tile_start, off_s, E, P.N);
+      const Tile T = decode_tile<NT>(t, tile_start, off_s, E, P.N);
       const uint8_t* base = P.a_scales + static_cast<size_t>(T.row0 + lane) * (P.K / 32);
       auto fetch = [&](int kb0, uint4 (&w)[G][2]) {
 #pragma unroll
@@ -233,7 +395,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_mx_gemm(const __grid_constant__
     const uint64_t da0 = desc_sw128(smem_u32(smem)), db0 = desc_sw128(smem_u32(smem + C::OFF_B));
     const uint64_t dsa0 = desc_plain(smem_u32(smem + C::OFF_SA)), dsb0 = desc_plain(smem_u32(smem + C::OFF_SB));
     for (int t = blockIdx.x; t < tiles && ok; t += gridDim.x, ++tile) {
-      const Tile T = decode_tile<kM, NT>(t, tile_start, off_s, E, P.N);
+      const Tile T = decode_tile<NT>(t, tile_start, off_s, E, P.N);
       const uint32_t id0 = idesc_mxf4(T.nn, 0), id1 = idesc_mxf4(T.nn, 1);
       const bool two_rt = C::RT == 2 && T.nn > 128;
       const uint32_t shift = NT == 64 ? (T.n0 >> 5) & 2 : 0;  // second half of a 128-row scale tile
@@ -297,7 +459,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_mx_gemm(const __grid_constant__
     int tile = 0;
     bool ok = true;
     for (int t = blockIdx.x; t < tiles && ok; t += gridDim.x, ++tile) {
-      const Tile T = decode_tile<kM, NT>(t, tile_start, off_s, E, P.N);
+      const Tile T = decode_tile<NT>(t, tile_start, off_s, E, P.N);
       ok = warp_wait(acc_full(tile), (tile >> 1) & 1, abort_flag, P.status);
       if (!ok) break;
       tc_fence_after();
@@ -321,9 +483,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_mx_gemm(const __grid_constant__
         const int grp = last_first && half == 1 ? 4 - i : i;
         const int c = grp * 64;
         if (grp < groups && any) {
-          bad |= store_group<OUT>(
-              P.out, [&](int blk) { return P.out_scales + static_cast<size_t>(T.row0 + r) * (P.N / 64) + blk; }, tb + c,
-              smem + C::OFF_OUT + (warp - 4) * kStageOut, lane, T.row0 + 32 * q, T.nrows - 32 * q, T.n0 + c, P.N);
+          bad |= store_group<OUT>(P.out, P.out_scales, tb + c, smem + C::OFF_OUT + (warp - 4) * kStageOut, lane,
+                                  T.row0 + 32 * q, T.nrows - 32 * q, T.n0 + c, P.N);
         }
         if (kShared && i == half && half == (last_first ? 1 : 0)) freed();
       }
@@ -345,6 +506,30 @@ __global__ void __launch_bounds__(kThreads, 1) k_mx_gemm(const __grid_constant__
 }
 
 // ---- host side ----------------------------------------------------------------
+
+PFN_cuTensorMapEncodeTiled_v12000 get_encode() {
+  static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
+  static std::once_flag once;
+  std::call_once(once, [] {
+    void* p = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &p, cudaEnableDefault, &q) == cudaSuccess &&
+        q == cudaDriverEntryPointSuccess)
+      fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(p);
+  });
+  return fn;
+}
+
+// Codes: rows of bytes, 128B swizzle.
+bool encode_bytes(CUtensorMap* m, int rank, const void* base, const cuuint64_t* dims, const cuuint64_t* strides,
+                         const cuuint32_t* box) {
+  auto fn = get_encode();
+  if (!fn) return false;
+  const cuuint32_t es[3] = {1, 1, 1};
+  return fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, rank, const_cast<void*>(base), dims, strides, box, es,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
 
 template <int NT, int OUT>
 moe_status_t launch(const MxGemmArgs& a, cudaStream_t s) {
@@ -405,7 +590,6 @@ template <int OUT>
 moe_status_t launch_out(const MxGemmArgs& a, cudaStream_t s) {
   // Widest weight tile that still gives every SM one: wide tiles read the
   // rows fewer times, narrow ones spread a small call's weights over more SMs.
-  if (a.paired) return launch_mx_pair(a, s);
   const long mt = std::max<long>(std::min(a.E, a.rows), a.rows / kM);
   if (mt * (a.N / 256) >= 148) return launch<256, OUT>(a, s);
   if (mt * (a.N / 128) >= 148) return launch<128, OUT>(a, s);
@@ -458,14 +642,6 @@ moe_status_t check(const char* fn, const void* codes, const void* scales, const 
 
 size_t up256(size_t n) { return (n + 255) / 256 * 256; }
 
-// Two SMs to a tile of 256 rows: where experts have that many rows on average
-// and every pair of SMs gets a tile (fewer rows would leave half of the pair's
-// products unused).
-constexpr int kPairRows = 192;
-bool paired(int rows, int E, int N) {
-  return rows > 0 && rows / std::min(E, rows) >= kPairRows && static_cast<long>(rows) / 256 * (N / 256) >= 74;
-}
-
 }  // namespace
 }  // namespace moeq
 
@@ -473,29 +649,14 @@ using namespace moeq;
 
 extern "C" {
 
-size_t moe_mx_gemm_workspace_bytes(int rows, int E, int N, int K) {
-  if (rows <= 0 || E <= 0 || N <= 0 || K <= 0 || !paired(rows, E, N)) return 0;
-  return mx_tiled_bytes(rows, E, K);
-}
-
 moe_status_t moe_mx_grouped_gemm(const void* codes, const void* scales, const int32_t* offsets, const void* mats,
-                                 int rows, int E, int N, int K, int out_dtype, void* out, void* workspace,
-                                 size_t workspace_bytes, int32_t* status, moe_stream_t stream) {
+                                 int rows, int E, int N, int K, int out_dtype, void* out, int32_t* status,
+                                 moe_stream_t stream) {
   const char* fn = "moe_mx_grouped_gemm";
-  moe_status_t st = check(fn, codes, scales, offsets, mats, out, rows, E, N, K);
+  const moe_status_t st = check(fn, codes, scales, offsets, mats, out, rows, E, N, K);
   if (st != MOE_OK) return st;
   if (out_dtype != MOE_F32 && out_dtype != MOE_BF16 && out_dtype != MOE_F16) {
     set_error("%s: unknown output dtype %d", fn, out_dtype);
-    return MOE_ERR_INVALID_ARG;
-  }
-  if (rows == 0) return MOE_OK;
-  const size_t need = moe_mx_gemm_workspace_bytes(rows, E, N, K);
-  if (need && (!workspace || workspace_bytes < need)) {
-    set_error("%s: workspace %zu < %zu bytes", fn, workspace_bytes, need);
-    return MOE_ERR_WORKSPACE;
-  }
-  if (need && !aligned16(workspace)) {
-    set_error("%s: workspace must be 16-byte aligned", fn);
     return MOE_ERR_INVALID_ARG;
   }
   MxGemmArgs a{};
@@ -511,23 +672,13 @@ moe_status_t moe_mx_grouped_gemm(const void* codes, const void* scales, const in
   a.out_kind = out_dtype == MOE_F32 ? kMxOutF32 : out_dtype == MOE_BF16 ? kMxOutBf16 : kMxOutF16;
   a.out = out;
   a.status = status;
-  a.paired = need != 0;
-  if (a.paired) {
-    st = launch_mx_tile_scales(a.a_scales, offsets, rows, E, K, static_cast<uint8_t*>(workspace),
-                               static_cast<cudaStream_t>(stream));
-    if (st != MOE_OK) return st;
-    a.a_tiles = static_cast<const uint8_t*>(workspace);
-  }
   return launch_mx_gemm(a, static_cast<cudaStream_t>(stream));
 }
 
-// Codes of h, its scales, and (two SMs to a tile) the rows' scales in tiles.
-size_t moe_ffn_mx_workspace_bytes(int rows, int E, int d, int F) {
-  if (rows <= 0 || E <= 0 || d <= 0 || F <= 0) return 256;
-  const size_t hc = up256(static_cast<size_t>(rows) * (F / 2));
-  const size_t flat = up256(static_cast<size_t>(rows) * (F / 32));
-  if (!paired(rows, E, 2 * F) || !paired(rows, E, d)) return hc + flat;
-  return hc + std::max(flat, up256(mx_tiled_bytes(rows, E, F))) + mx_tiled_bytes(rows, E, d);
+// Codes of h, then its scales.
+size_t moe_ffn_mx_workspace_bytes(int rows, int F) {
+  if (rows <= 0 || F <= 0) return 256;
+  return up256(static_cast<size_t>(rows) * (F / 2)) + up256(static_cast<size_t>(rows) * (F / 32));
 }
 
 moe_status_t moe_grouped_ffn_mx(const void* codes, const void* scales, const int32_t* offsets, const void* blobs,
@@ -538,7 +689,7 @@ moe_status_t moe_grouped_ffn_mx(const void* codes, const void* scales, const int
   if (st == MOE_OK) st = check(fn, codes, scales, offsets, blobs, y_perm, rows, E, 2 * F, d);
   if (st != MOE_OK) return st;
   if (rows == 0) return MOE_OK;
-  const size_t need = moe_ffn_mx_workspace_bytes(rows, E, d, F);
+  const size_t need = moe_ffn_mx_workspace_bytes(rows, F);
   if (!workspace || workspace_bytes < need) {
     set_error("%s: workspace %zu < %zu bytes", fn, workspace_bytes, need);
     return MOE_ERR_WORKSPACE;
@@ -563,18 +714,10 @@ moe_status_t moe_grouped_ffn_mx(const void* codes, const void* scales, const int
   a.out = hc;
   a.out_scales = hs;
   a.status = status;
-  a.paired = paired(rows, E, 2 * F) && paired(rows, E, d);
-  if (a.paired) {
-    uint8_t* xs = static_cast<uint8_t*>(workspace) + need - mx_tiled_bytes(rows, E, d);
-    st = launch_mx_tile_scales(a.a_scales, offsets, rows, E, d, xs, static_cast<cudaStream_t>(stream));
-    if (st != MOE_OK) return st;
-    a.a_tiles = xs;
-  }
   st = launch_mx_gemm(a, static_cast<cudaStream_t>(stream));
   if (st != MOE_OK) return st;
   a.a_codes = hc;
   a.a_scales = hs;
-  a.a_tiles = hs;
   a.mats = static_cast<const uint8_t*>(blobs) + mx_matrix_bytes(2 * F, d);
   a.N = d;
   a.K = F;

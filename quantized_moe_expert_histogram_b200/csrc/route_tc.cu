@@ -124,7 +124,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_route_tc(const __grid_constant_
   auto empty = [&](int i) { return bar0 + 8u * (kStages + i); };
   const uint32_t hi_full = bar0 + 8u * (2 * kStages), hi_free = hi_full + 8u, ml_full = hi_free + 8u;
   const uint32_t exit_bar = ml_full + 8u, drain_bar = exit_bar + 8u;
-  const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int t0 = blockIdx.x * kT, e0 = blockIdx.y * kE, split = blockIdx.z;
   const int c0 = split * P.per_split, n = max(0, min(P.per_split, P.chunks - c0));
   const bool norms = blockIdx.y == 0;  // this CTA also sums the squares of its tokens' slices

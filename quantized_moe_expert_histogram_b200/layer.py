@@ -121,7 +121,7 @@ class MxMoELayer:
             status=torch.zeros(1, dtype=torch.int32, device=dev),
             route_ws=torch.empty(moeq.moe_route_scored_workspace_bytes(T, d, E), dtype=torch.uint8, device=dev),
             perm_ws=torch.empty(moeq.moe_permute_workspace_bytes(T, E, k, False), dtype=torch.uint8, device=dev),
-            workspace=torch.empty(moeq.moe_ffn_mx_workspace_bytes(rows, E, d, F), dtype=torch.uint8, device=dev),
+            workspace=torch.empty(moeq.moe_ffn_mx_workspace_bytes(rows, F), dtype=torch.uint8, device=dev),
         )
 
     @classmethod

@@ -62,11 +62,9 @@ _SIGS = {
     "moe_mx_dequantize": (_c_i, [_c_p, _c_p, _c_i, _c_i, _c_i, _c_p, _c_p]),
     "moe_mx_pack": (_c_i, [_c_p, _c_i, _c_i, _c_i, _c_i, _c_p, _c_p, _c_p]),
     "moe_mx_pack_ffn": (_c_i, [_c_p, _c_p, _c_p, _c_i, _c_i, _c_i, _c_i, _c_p, _c_p, _c_p]),
-    "moe_mx_grouped_gemm": (_c_i, [_c_p, _c_p, _c_p, _c_p, _c_i, _c_i, _c_i, _c_i, _c_i, _c_p, _c_p, _c_sz, _c_p,
-                                   _c_p]),
-    "moe_mx_gemm_workspace_bytes": (_c_sz, [_c_i, _c_i, _c_i, _c_i]),
+    "moe_mx_grouped_gemm": (_c_i, [_c_p, _c_p, _c_p, _c_p, _c_i, _c_i, _c_i, _c_i, _c_i, _c_p, _c_p, _c_p]),
     "moe_grouped_ffn_mx": (_c_i, [_c_p, _c_p, _c_p, _c_p, _c_i, _c_i, _c_i, _c_i, _c_p, _c_sz, _c_p, _c_p, _c_p]),
-    "moe_ffn_mx_workspace_bytes": (_c_sz, [_c_i, _c_i, _c_i, _c_i]),
+    "moe_ffn_mx_workspace_bytes": (_c_sz, [_c_i, _c_i]),
     "moe_slot_cache_create": (_c_i, [_c_i, _c_i, _c_sz, _c_p, _c_p, ctypes.POINTER(_c_p)]),
     "moe_slot_cache_create_planes": (_c_i, [_c_i, _c_i, _c_i, _c_i, _c_i, _c_p, _c_p, ctypes.POINTER(_c_p)]),
     "moe_slot_stage": (_c_i, [_c_p, _c_p, _c_p, _c_i, _c_p, _c_p, _c_p, _c_p]),
@@ -556,35 +554,25 @@ def _mx_args(fn, codes, scales, offsets, mats, nbytes):
     return rows, K, E
 
 
-def moe_mx_gemm_workspace_bytes(rows, E, N, K):
-    return int(load().moe_mx_gemm_workspace_bytes(rows, E, N, K))
-
-
-def moe_mx_grouped_gemm(codes, scales, offsets, mats, N, dtype=torch.float16, out=None, workspace=None, status=None,
-                        stream=None):
+def moe_mx_grouped_gemm(codes, scales, offsets, mats, N, dtype=torch.float16, out=None, status=None, stream=None):
     """y[p] = W_e xq[p] for the rows of each expert; returns [rows][N] in dtype."""
     lib = load()
     fn = "moe_mx_grouped_gemm"
     dt = _dtype_id(fn, "dtype", dtype)
     rows, K, E = _mx_args(fn, codes, scales, offsets, mats, lib.moe_mx_matrix_bytes(N, codes.shape[1] * 2))
     _sized(fn, "out", out, (rows, N))
-    with _on(fn, codes, scales, offsets, mats, out, workspace, status):
+    with _on(fn, codes, scales, offsets, mats, out, status):
         if out is None:
             out = codes.new_empty((rows, N), dtype=dtype)
-        if workspace is None:
-            need = lib.moe_mx_gemm_workspace_bytes(rows, E, N, K)
-            workspace = codes.new_empty((need,)) if need else None
         _check(fn, lib.moe_mx_grouped_gemm(
             _ptr(codes, torch.uint8, "codes"), _ptr(scales, torch.uint8, "scales"),
             _ptr(offsets, torch.int32, "offsets"), _ptr(mats, torch.uint8, "mats"), rows, E, N, K, dt,
-            _ptr(out, dtype, "out"), _ptr(workspace),
-            0 if workspace is None else workspace.numel() * workspace.element_size(),
-            _ptr(status, torch.int32, "status"), _stream(stream)))
+            _ptr(out, dtype, "out"), _ptr(status, torch.int32, "status"), _stream(stream)))
     return out
 
 
-def moe_ffn_mx_workspace_bytes(rows, E, d, F):
-    return int(load().moe_ffn_mx_workspace_bytes(rows, E, d, F))
+def moe_ffn_mx_workspace_bytes(rows, F):
+    return int(load().moe_ffn_mx_workspace_bytes(rows, F))
 
 
 def moe_grouped_ffn_mx(codes, scales, offsets, blobs, F, workspace=None, y_perm=None, status=None, stream=None):
@@ -595,7 +583,7 @@ def moe_grouped_ffn_mx(codes, scales, offsets, blobs, F, workspace=None, y_perm=
     _sized(fn, "y_perm", y_perm, (rows, d))
     with _on(fn, codes, scales, offsets, blobs, workspace, y_perm, status):
         if workspace is None:
-            workspace = codes.new_empty((lib.moe_ffn_mx_workspace_bytes(rows, E, d, F),))
+            workspace = codes.new_empty((lib.moe_ffn_mx_workspace_bytes(rows, F),))
         if y_perm is None:
             y_perm = codes.new_empty((rows, d), dtype=torch.float16)
         _check(fn, lib.moe_grouped_ffn_mx(

@@ -185,8 +185,7 @@ def test_grouped_gemm(rows_of, N, K, dtype):
     ([200] * 64, 384, 256),                 # 256 outputs a tile, the last one half
     ([1300, 5, 0, 700], 2560, 1152),        # 256 outputs a tile, several row tiles, half a last K stage
     ([2] * 100, 128, 2048),
-    # two SMs to a tile of 256 rows
-    ([300] * 12, 2048, 384),                # a full and a short row tile each, half a last K stage
+    ([300] * 12, 2048, 384),                # full and short row tiles, half a last K stage
     ([700, 0, 1, 900], 3456, 640),          # the last 128 outputs alone, one row, no row
     ([2600], 2048, 2304),                   # many stages
 ])
@@ -237,7 +236,7 @@ def ffn_weights(E, d, F, seed=50):
 
 @pytest.mark.parametrize("rows_of,d,F", [([1], 128, 128), ([0, 3, 0, 140], 256, 384), ([9, 128, 1], 384, 256),
                                          ([1, 1, 0, 2, 1, 1, 1, 1], 512, 512), ([260] * 12, 256, 2048),
-                                         # two SMs to a tile in both products
+                                         # 256 outputs a tile in both products
                                          ([400, 129, 0, 500, 1, 700], 2432, 1536)])
 def test_ffn(rows_of, d, F):
     E, R = len(rows_of), int(sum(rows_of))
@@ -265,7 +264,7 @@ def test_calls_repeat_bit_for_bit_and_in_a_graph():
     off = table(rows_of)
     x = normal(R, d, seed=71, dtype=torch.bfloat16)
     codes, scales = moeq.moe_mx_quantize(x)
-    ws = torch.empty(moeq.moe_ffn_mx_workspace_bytes(R, 4, d, F), dtype=torch.uint8, device="cuda")
+    ws = torch.empty(moeq.moe_ffn_mx_workspace_bytes(R, F), dtype=torch.uint8, device="cuda")
     first = moeq.moe_grouped_ffn_mx(codes, scales, off, blobs, F)
     y = torch.zeros_like(first)
     s = torch.cuda.Stream()

@@ -60,8 +60,8 @@ def test_dequantize_and_pack_refuse(lib):
     assert lib.moe_mx_pack_ffn(P, None, P, 0, 2, 128, 128, P, None, None) == INVALID
 
 
-def gemm(L, rows=8, E=4, N=128, K=128, dtype=2, codes=P, scales=P, off=P, mats=P, out=P, ws=None, nbytes=0):
-    return L.moe_mx_grouped_gemm(codes, scales, off, mats, rows, E, N, K, dtype, out, ws, nbytes, None, None)
+def gemm(L, rows=8, E=4, N=128, K=128, dtype=2, codes=P, scales=P, off=P, mats=P, out=P):
+    return L.moe_mx_grouped_gemm(codes, scales, off, mats, rows, E, N, K, dtype, out, None, None)
 
 
 def ffn(L, rows=8, E=4, d=128, F=128, ws=P, nbytes=1 << 20, codes=P, out=P):
@@ -73,9 +73,6 @@ def ffn(L, rows=8, E=4, d=128, F=128, ws=P, nbytes=1 << 20, codes=P, out=P):
     (dict(K=96), SHAPE, "128"), (dict(E=257), SHAPE, "256"), (dict(dtype=5), INVALID, "dtype"),
     (dict(codes=None), INVALID, "null"), (dict(off=None), INVALID, "null"), (dict(out=P + 2), INVALID, "aligned"),
     (dict(scales=P + 8), INVALID, "aligned"), (dict(rows=2 ** 31 - 1, N=1 << 24), SHAPE, "tiles"),
-    (dict(rows=4096, E=1, N=4096, K=4096), WORKSPACE, "workspace"),
-    (dict(rows=4096, E=1, N=4096, K=4096, ws=P, nbytes=1000), WORKSPACE, "workspace"),
-    (dict(rows=4096, E=1, N=4096, K=4096, ws=P + 8, nbytes=1 << 30), INVALID, "aligned"),
 ])
 def test_grouped_gemm_refuses(lib, args, code, words):
     assert gemm(lib, **args) == code
@@ -105,13 +102,6 @@ def test_sizes(lib):
     for N, K in ((0, 128), (128, 100), (-128, 128)):
         assert lib.moe_mx_matrix_bytes(N, K) == 0
     assert lib.moe_mx_blob_bytes(128, 64) == 0
-    assert lib.moe_ffn_mx_workspace_bytes(3, 4, 128, 128) == 256 + 256
-    assert lib.moe_ffn_mx_workspace_bytes(0, 4, 128, 128) == 256
-    assert lib.moe_mx_gemm_workspace_bytes(8, 4, 128, 128) == 0
-    assert lib.moe_mx_gemm_workspace_bytes(4096, 1, 4096, 4096) == 33 * 32 * 512
-    for E, d, F in ((1, 4096, 4096), (8, 4096, 14336), (64, 2048, 1024), (256, 128, 128)):   # the largest batch's serves all
-        rows = (1, 5, 64, 300, 1000, 2048, 4096, 5000, 12288, 20000, 32768, 100000)
-        for sizes in ([lib.moe_ffn_mx_workspace_bytes(r, E, d, F) for r in rows],
-                      [lib.moe_mx_gemm_workspace_bytes(r, E, d, F) for r in rows]):
-            assert sizes == sorted(sizes)
+    assert lib.moe_ffn_mx_workspace_bytes(3, 128) == 256 + 256
+    assert lib.moe_ffn_mx_workspace_bytes(0, 128) == 256
     assert lib.moe_route_scored_workspace_bytes(0, 256, 64) >= 256
