@@ -56,7 +56,7 @@ constexpr int kM = 128;       // rows of a tile
 constexpr int kKS = 256;      // K of a stage (128 bytes of codes)
 constexpr int kABox = 32;     // rows of one activation box
 constexpr int kEpiWarps = 8;
-constexpr int kStageOut = 1024;  // staging bytes of an epilogue warp: 32 rows x 32 bytes
+constexpr int kStageOut = 2048;  // staging bytes of an epilogue warp: 32 rows x 64 bytes
 
 constexpr int kNT = 256;      // outputs of a tile (half tiles: 128)
 constexpr int kStages = 4;
@@ -205,28 +205,27 @@ __device__ __forceinline__ bool store_group(void* out_v, uint8_t* out_scales, ui
     }
     return bad;
   }
-  // 32 bytes of every row at a time through the warp's staging rows (16-byte
-  // pieces swapped by row), so that a store instruction covers whole sectors
-  constexpr int ES = OUT == kMxOutF32 ? 4 : 2, CW = 32 / ES;
-  uint8_t* out = static_cast<uint8_t*>(out_v) + (static_cast<size_t>(row0) * N + n0) * ES + (lane & 1) * 16;
-  uint32_t v[32];
+  // 64 bytes of every row at a time through the warp's staging rows (16-byte
+  // pieces swizzled by row), so that a store instruction covers whole 64-byte
+  // runs
+  constexpr int ES = OUT == kMxOutF32 ? 4 : 2, CW = 64 / ES;
+  uint8_t* out = static_cast<uint8_t*>(out_v) + (static_cast<size_t>(row0 + (lane >> 2)) * N + n0) * ES + (lane & 3) * 16;
+  uint32_t v[64];
+  tmem_ld32(taddr, *reinterpret_cast<uint32_t(*)[32]>(v));
+  tmem_ld32(taddr + 32, *reinterpret_cast<uint32_t(*)[32]>(v + 32));
+  tmem_ld_wait();
 #pragma unroll
   for (int c = 0; c < 64; c += CW) {
-    if (c % 32 == 0) {
-      tmem_ld32(taddr + c, v);
-      tmem_ld_wait();
-    }
     __syncwarp();  // the rows staged before have been read
 #pragma unroll
-    for (int j = 0; j < 2; ++j) {
+    for (int j = 0; j < 4; ++j) {
       uint32_t w[4];
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
         if (OUT == kMxOutF32) {
-          w[k] = v[c % 32 + 4 * j + k];
+          w[k] = v[c + 4 * j + k];
         } else {
-          const float y0 = __uint_as_float(v[c % 32 + 8 * j + 2 * k]);
-          const float y1 = __uint_as_float(v[c % 32 + 8 * j + 2 * k + 1]);
+          const float y0 = __uint_as_float(v[c + 8 * j + 2 * k]), y1 = __uint_as_float(v[c + 8 * j + 2 * k + 1]);
           if (OUT == kMxOutF16) {
             bad |= !(fabsf(y0) <= 65504.0f) || !(fabsf(y1) <= 65504.0f);
             const __half2 h = __floats2half2_rn(y0, y1);
@@ -237,16 +236,19 @@ __device__ __forceinline__ bool store_group(void* out_v, uint8_t* out_scales, ui
           }
         }
       }
-      *reinterpret_cast<uint4*>(st + lane * 32 + ((j ^ ((lane >> 2) & 1)) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
+      *reinterpret_cast<uint4*>(st + lane * 64 + ((j ^ ((lane >> 1) & 3)) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
     }
     __syncwarp();
+    uint4 t[4];
 #pragma unroll
-    for (int k = 0; k < 2; ++k) {
-      const int row = 16 * k + (lane >> 1);
-      if (row < live)
-        *reinterpret_cast<uint4*>(out + (static_cast<size_t>(row) * N + c) * ES) =
-            *reinterpret_cast<const uint4*>(st + row * 32 + (((lane & 1) ^ ((row >> 2) & 1)) << 4));
+    for (int k = 0; k < 4; ++k) {
+      const int row = 8 * k + (lane >> 2);
+      t[k] = *reinterpret_cast<const uint4*>(st + row * 64 + (((lane & 3) ^ ((row >> 1) & 3)) << 4));
     }
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+      if (8 * k + (lane >> 2) < live)
+        *reinterpret_cast<uint4*>(out + (static_cast<size_t>(8 * k) * N + c) * ES) = t[k];
   }
   return bad && lane < live;
 }
