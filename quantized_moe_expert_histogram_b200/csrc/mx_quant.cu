@@ -9,8 +9,14 @@
 //
 // Rows in expert order: a token's row is quantised once and its codes are
 // written to the k places inv_perm names, so x is read once and the
-// arithmetic is done once per token, not per assignment.  Bound: HBM writes
-// (17/32 byte per element and assignment).
+// arithmetic is done once per token, not per assignment.  Bound: HBM (reads of
+// x, writes of 17/32 byte per element and assignment).
+//
+// A block's work is one pass (a persistent grid of 8 blocks an SM took 6 to 8 %
+// longer), and what is used once goes through the caches as streaming: fp32
+// rows in (134.0 -> 125.5 us for 28673 x 4096 to MXFP4 and back), bf16 values
+// out (41.5 -> 35.2 us for 4096 x 2048 to 8 places and back).  That is 93 % and
+// 81 % of the copy bandwidth.
 #include "mx.cuh"
 
 namespace moeq {
@@ -20,9 +26,10 @@ constexpr int kPiece = 256;  // elements of one warp-wide load
 constexpr int kPieces = 4;
 constexpr int kChunk = kPiece * kPieces;
 constexpr int kThreads = 256;
+constexpr int kValuesPerBlock = 4 * kThreads;  // words of 8 codes a block of k_mx_values takes
 
 __device__ __forceinline__ void load8(const float* p, float (&v)[8]) {
-  const float4 a = reinterpret_cast<const float4*>(p)[0], b = reinterpret_cast<const float4*>(p)[1];
+  const float4 a = __ldcs(reinterpret_cast<const float4*>(p)), b = __ldcs(reinterpret_cast<const float4*>(p) + 1);
   v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
   v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
 }
@@ -177,7 +184,7 @@ __device__ __forceinline__ void store8(__nv_bfloat16* p, const float (&v)[8]) {
   __nv_bfloat162* h = reinterpret_cast<__nv_bfloat162*>(&r);
 #pragma unroll
   for (int j = 0; j < 4; ++j) h[j] = __floats2bfloat162_rn(v[2 * j], v[2 * j + 1]);
-  *reinterpret_cast<uint4*>(p) = r;
+  __stcs(reinterpret_cast<uint4*>(p), r);
 }
 
 // A thread turns 8 codes into 8 values; four words in flight per thread.
@@ -187,7 +194,7 @@ __global__ void __launch_bounds__(kThreads) k_mx_values(const uint8_t* __restric
                                                         T* __restrict__ out) {
   pdl_wait();
   pdl_trigger();
-  constexpr int U = 4;
+  constexpr int U = kValuesPerBlock / kThreads;
   const long step = static_cast<long>(gridDim.x) * kThreads * U;
   for (long i0 = static_cast<long>(blockIdx.x) * kThreads * U + threadIdx.x; i0 < words; i0 += step) {
     uint32_t w[U], b[U];
@@ -211,8 +218,8 @@ __global__ void __launch_bounds__(kThreads) k_mx_values(const uint8_t* __restric
   }
 }
 
-int blocks_for(long warps_of_work) {
-  return static_cast<int>(std::max<long>(1, std::min<long>((warps_of_work + kThreads / 32 - 1) / (kThreads / 32), 148L * 8)));
+int blocks_for(long work, long per_block) {
+  return static_cast<int>(std::min<long>((work + per_block - 1) / per_block, 1L << 30));
 }
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
@@ -223,7 +230,7 @@ template <typename T>
 cudaError_t pack_one(const void* w, int E, int n_rows, int K, int mode, int N, uint8_t* out, size_t stride,
                      int32_t* status, cudaStream_t s) {
   const long items = static_cast<long>(E) * n_rows * ((K + kChunk - 1) / kChunk);
-  return launch_pdl(false, k_mx_pack<T>, dim3(blocks_for(items)), dim3(kThreads), 0, s, static_cast<const T*>(w), E,
+  return launch_pdl(false, k_mx_pack<T>, dim3(blocks_for(items, kThreads / 32)), dim3(kThreads), 0, s, static_cast<const T*>(w), E,
                     n_rows, K, mode, N, out, stride, status);
 }
 
@@ -283,7 +290,7 @@ moe_status_t moe_mx_quantize(const void* x, int dtype, int rows, int K, size_t l
     return MOE_ERR_INVALID_ARG;
   }
   const long items = static_cast<long>(rows) * ((K + kChunk - 1) / kChunk);
-  const dim3 grid(blocks_for(items)), block(kThreads);
+  const dim3 grid(blocks_for(items, kThreads / 32)), block(kThreads);
   const bool pdl = pdl_for(static_cast<long>(rows) * k);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   uint8_t* c = static_cast<uint8_t*>(codes);
@@ -323,7 +330,7 @@ moe_status_t moe_mx_dequantize(const void* codes, const void* scales, int rows, 
     return MOE_ERR_INVALID_ARG;
   }
   const long words = static_cast<long>(rows) * (K / 8);
-  const dim3 grid(blocks_for((words + 127) / 128)), block(kThreads);
+  const dim3 grid(blocks_for(words, kValuesPerBlock)), block(kThreads);
   const bool pdl = pdl_for(rows);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   const uint8_t* c = static_cast<const uint8_t*>(codes);
