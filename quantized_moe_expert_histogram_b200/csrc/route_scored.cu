@@ -21,8 +21,9 @@
 // evaluated whole.
 //
 // Carrying the bound (u = 2^-24): sigmoid' = s (1 - s), and over an interval
-// of half width D <= 0.05 it grows by at most e^0.05 < 1.06; expf (2 ulp), the
-// sum and the division (2 ulp each) err by less than 12 u s, the bias addition by u |c|.
+// of half width D <= 0.05 it grows by at most e^0.05 < 1.06; __expf errs by (2 +
+// 1.2 |l|) 2^-23 relative, of which s feels the part 1 - s, the sum and the
+// division (2 ulp) by less than 6 u s, the bias addition by u |c|.
 // Softmax: every numerator and the denominator err by a relative
 // 2 D_max + 4 u (|l - max|) + (E / 32 + 20) u at most, D_max <= 0.05.
 #include "common.cuh"
@@ -55,6 +56,13 @@ struct Row {
   int n;
   int raw;  // v holds logits
 };
+
+// 2^-23 relative (the bounds have 2^-8 to spare for the norms).
+__device__ __forceinline__ float sqrt_approx(float v) {
+  float r;
+  asm("sqrt.approx.f32 %0, %1;" : "=f"(r) : "f"(v));
+  return r;
+}
 
 // NaN counts as -inf.
 __device__ __forceinline__ double ordered(double v) { return v == v ? v : -INFINITY; }
@@ -256,8 +264,8 @@ __device__ __forceinline__ void select_block(const Scored& A, Row<P>* rows, int 
         const float b = A.bias ? A.bias[e] : 0.f;
         float s, ds;
         if (A.sigmoid) {
-          s = __fdividef(1.0f, 1.0f + expf(-L[m]));
-          ds = 1.06f * D[m] * (s * (1.0f - s) + 2.0e-7f) + 7.0e-7f * s;
+          s = __fdividef(1.0f, 1.0f + __expf(-L[m]));
+          ds = (1.06f * D[m] + 1.2e-7f * (2.0f + 1.2f * fabsf(L[m]))) * (s * (1.0f - s) + 2.0e-7f) + 4.0e-7f * s;
         } else {
           s = __fdividef(expf(L[m] - row_max), row_sum);
           ds = s * (2.2f * d_max + 2.4e-7f * (row_max - L[m]) + 6.0e-8f * (E / 32 + 20)) * 1.06f;
@@ -402,18 +410,18 @@ __device__ __forceinline__ void select_block(const Scored& A, Row<P>* rows, int 
       for (int m = 0; m < P; ++m)
         if (!((group_in >> min((lane + 32 * m) / gs, 31)) & 1u)) allowed &= ~(1u << m);
     }
-    uint32_t left = allowed;
+    uint32_t left = allowed, key[P];
+#pragma unroll
+    for (int m = 0; m < P; ++m) key[m] = order_key(C[m]);
     for (int j = 0; j < k; ++j) {
       uint32_t bk = 0;
       int be = 0x7fffffff;
 #pragma unroll
-      for (int m = 0; m < P; ++m) {
-        const uint32_t key = order_key(C[m]);
-        if (((left >> m) & 1u) && key > bk) {  // the lane's lowest expert on equal keys
-          bk = key;
+      for (int m = 0; m < P; ++m)
+        if (((left >> m) & 1u) && key[m] > bk) {  // the lane's lowest expert on equal keys
+          bk = key[m];
           be = lane + 32 * m;
         }
-      }
       const uint32_t top = __reduce_max_sync(0xffffffffu, bk);
       const int e = __reduce_min_sync(0xffffffffu, bk == top ? be : 0x7fffffff);
       if ((e & 31) == lane) left &= ~(1u << (e >> 5));
@@ -577,10 +585,10 @@ __global__ void __launch_bounds__(kThreads, 3) k_route_scored(const __grid_const
 #pragma unroll
       for (int m = 0; m < P; ++m)
         if (lane + 32 * m < E) wq[m] += A.lg.wsq[static_cast<size_t>(s) * E + lane + 32 * m];
-    const float xn = sqrtf(xq);
+    const float xn = sqrt_approx(xq);
 #pragma unroll
     for (int m = 0; m < P; ++m) {
-      const float wn = sqrtf(wq[m]);
+      const float wn = sqrt_approx(wq[m]);
       D[m] = A.lg.gamma * xn * wn * (1.0f + 0.00390625f) + 1.2e-7f * fabsf(L[m]) + 5e-37f * (xn + wn) + 1e-30f;
     }
   });
