@@ -212,8 +212,8 @@ MOE_API moe_status_t moe_route_topk_noalloc(const void* x, const float* w_router
  *   status    device word or NULL: MOE_DEV_TIMEOUT when a bounded wait ran out
  *             (the outputs are then undefined).
  * topk_idx and topk_w are what moe_permute and moe_unpermute_combine take.
- * Requires 1 <= k <= E <= 256, k <= 16, d % 32 == 0, n_groups <= 32 dividing
- * E, group_top experts or more to a group and k or more in the groups that
+ * Requires 1 <= k <= E <= 256, k <= 16, d % 32 == 0, d <= 32768, n_groups <= 32
+ * dividing E, group_top experts or more to a group and k or more in the groups that
  * stay. */
 typedef enum { MOE_SCORE_SOFTMAX = 0, MOE_SCORE_SIGMOID = 1 } moe_scoring_t;
 MOE_API moe_status_t moe_route_scored(const void* x, const float* w_router, const float* bias, int T, int d, int E,
@@ -404,7 +404,8 @@ MOE_API size_t moe_mx_blob_bytes(int d, int F);
  *   codes    [rows * k][K/2], scales [rows * k][K/32]
  * Places outside [0, rows * k) are skipped and flag MOE_DEV_BAD_INDEX in
  * `status` (may be NULL); output rows that no place names keep what they
- * held.  Requires K % 32 == 0, rows a multiple of 16 bytes apart, x and codes
+ * held (places are distinct, as moe_permute's are: a row named twice holds a
+ * mixture).  Requires K % 32 == 0, rows a multiple of 16 bytes apart, x and codes
  * 16-byte aligned, rows * k < 2^31. */
 MOE_API moe_status_t moe_mx_quantize(const void* x, int dtype, int rows, int K, size_t ld, const int32_t* inv_perm,
                                      int k, void* codes, void* scales, int32_t* status, moe_stream_t stream);

@@ -589,7 +589,7 @@ __global__ void __launch_bounds__(kThreads, 3) k_route_scored(const __grid_const
 #pragma unroll
     for (int m = 0; m < P; ++m) {
       const float wn = sqrt_approx(wq[m]);
-      D[m] = A.lg.gamma * xn * wn * (1.0f + 0.00390625f) + 1.2e-7f * fabsf(L[m]) + 5e-37f * (xn + wn) + 1e-30f;
+      D[m] = A.lg.gamma * xn * wn * (1.0f + 0.00390625f) + 1.2e-7f * fabsf(L[m]) + 7e-36f * (xn + wn) + 1e-30f;
     }
   });
 }
@@ -664,6 +664,10 @@ moe_status_t moe_route_scored(const void* x, const float* w_router, const float*
   const char* fn = "moe_route_scored";
   moe_status_t st = route_check_args(x, w_router, T, d, E, k, topk_idx, topk_w, fn);
   if (st != MOE_OK) return st;
+  if (d > 32768) {
+    set_error("%s: d=%d exceeds 32768 (the logits' error bounds)", fn, d);
+    return MOE_ERR_UNSUPPORTED_SHAPE;
+  }
   if (scoring != MOE_SCORE_SOFTMAX && scoring != MOE_SCORE_SIGMOID) {
     set_error("%s: unknown scoring %d", fn, scoring);
     return MOE_ERR_INVALID_ARG;

@@ -15,9 +15,9 @@
 // chunks = d / 64 and S slices of d:
 //   |L - l| <= |x| |W_e| (64 2^-23 + (chunks + S + 2) 2^-24
 //                         + 2 d 2^-23 2^-9 1.01 + 2^-26)
-// and the select kernel takes 1.1 times that (second-order terms).  Parts
-// that are subnormal in bf16 may count as zero: 2^-126 each, which the select
-// kernel's absolute term covers for values in range.
+// and the select kernel takes 1.1 times that (second-order terms).  Parts and
+// activations that are subnormal in bf16 may count as zero, 2^-126 each: at
+// most 2^-126 sqrt(d) (3 |x| + |W_e|), which the select kernel adds.
 //
 // A CTA computes 128 experts x 256 tokens of one slice of d: the experts are
 // the M side (a lane of tensor memory is an expert, so a warp's stores of

@@ -410,6 +410,15 @@ def _on(fn, first, *others):
     return _SAME if dev == torch.cuda.current_device() else _Other(dev)
 
 
+def _new(like, shape, dtype, stream):
+    """A new tensor on the device of `like`, for a call on `stream` (its memory
+    is not given out again before that stream has passed its release)."""
+    t = like.new_empty(shape, dtype=dtype)
+    if stream is not None:
+        t.record_stream(stream)
+    return t
+
+
 def _sized(fn, name, t, shape):
     if t is not None and t.shape != shape:
         raise ValueError(f"{fn}: {name} must have shape {shape}, got {tuple(t.shape)}")
@@ -441,11 +450,11 @@ def moe_route_scored(x, w_router, k, scoring="softmax", bias=None, n_groups=1, t
     _sized(fn, "topk_w", topk_w, (T, k))
     with _on(fn, x, w_router, bias, topk_idx, topk_w, workspace, status):
         if topk_idx is None:
-            topk_idx = x.new_empty((T, k), dtype=torch.int32)
+            topk_idx = _new(x, (T, k), torch.int32, stream)
         if topk_w is None:
-            topk_w = x.new_empty((T, k), dtype=torch.float32)
+            topk_w = _new(x, (T, k), torch.float32, stream)
         if workspace is None:
-            workspace = x.new_empty((lib.moe_route_scored_workspace_bytes(T, d, E),), dtype=torch.uint8)
+            workspace = _new(x, (lib.moe_route_scored_workspace_bytes(T, d, E),), torch.uint8, stream)
         _check(fn, lib.moe_route_scored(
             _ptr(x, torch.bfloat16, "x"), _ptr(w_router, torch.float32, "w_router"), _ptr(bias, torch.float32, "bias"),
             T, d, E, k, _SCORING[scoring], n_groups, topk_groups, group_top, 1 if renorm else 0, scale,
@@ -481,9 +490,9 @@ def moe_mx_quantize(x, inv_perm=None, k=1, codes=None, scales=None, status=None,
     _sized(fn, "scales", scales, (rows * k, K // 32))
     with _on(fn, x, inv_perm, codes, scales, status):
         if codes is None:
-            codes = x.new_empty((rows * k, K // 2), dtype=torch.uint8)
+            codes = _new(x, (rows * k, K // 2), torch.uint8, stream)
         if scales is None:
-            scales = x.new_empty((rows * k, K // 32), dtype=torch.uint8)
+            scales = _new(x, (rows * k, K // 32), torch.uint8, stream)
         _check(fn, lib.moe_mx_quantize(
             x.data_ptr(), dt, rows, K, ld, _ptr(inv_perm, torch.int32, "inv_perm"), k,
             _ptr(codes, torch.uint8, "codes"), _ptr(scales, torch.uint8, "scales"),
@@ -502,7 +511,7 @@ def moe_mx_dequantize(codes, scales, dtype=torch.bfloat16, out=None, stream=None
     _sized(fn, "out", out, (rows, K))
     with _on(fn, codes, scales, out):
         if out is None:
-            out = codes.new_empty((rows, K), dtype=dtype)
+            out = _new(codes, (rows, K), dtype, stream)
         _check(fn, lib.moe_mx_dequantize(_ptr(codes, torch.uint8, "codes"), _ptr(scales, torch.uint8, "scales"), rows,
                                          K, dt, _ptr(out, dtype, "out"), _stream(stream)))
     return out
@@ -518,7 +527,7 @@ def moe_mx_pack(w, mats=None, status=None, stream=None):
     _sized(fn, "mats", mats, (E, nb))
     with _on(fn, w, mats, status):
         if mats is None:
-            mats = w.new_empty((E, nb), dtype=torch.uint8)
+            mats = _new(w, (E, nb), torch.uint8, stream)
         _check(fn, lib.moe_mx_pack(_ptr(w, None, "w"), dt, E, N, K, _ptr(mats, torch.uint8, "mats") or None,
                                    _ptr(status, torch.int32, "status"), _stream(stream)))
     return mats
@@ -536,7 +545,7 @@ def moe_mx_pack_ffn(w_gate, w_up, w_down, blobs=None, status=None, stream=None):
     _sized(fn, "blobs", blobs, (E, nb))
     with _on(fn, w_gate, w_up, w_down, blobs, status):
         if blobs is None:
-            blobs = w_gate.new_empty((E, nb), dtype=torch.uint8)
+            blobs = _new(w_gate, (E, nb), torch.uint8, stream)
         _check(fn, lib.moe_mx_pack_ffn(
             _ptr(w_gate, None, "w_gate"), _ptr(w_up, w_gate.dtype, "w_up"), _ptr(w_down, w_gate.dtype, "w_down"), dt,
             E, d, F, _ptr(blobs, torch.uint8, "blobs") or None, _ptr(status, torch.int32, "status"), _stream(stream)))
@@ -563,7 +572,7 @@ def moe_mx_grouped_gemm(codes, scales, offsets, mats, N, dtype=torch.float16, ou
     _sized(fn, "out", out, (rows, N))
     with _on(fn, codes, scales, offsets, mats, out, status):
         if out is None:
-            out = codes.new_empty((rows, N), dtype=dtype)
+            out = _new(codes, (rows, N), dtype, stream)
         _check(fn, lib.moe_mx_grouped_gemm(
             _ptr(codes, torch.uint8, "codes"), _ptr(scales, torch.uint8, "scales"),
             _ptr(offsets, torch.int32, "offsets"), _ptr(mats, torch.uint8, "mats"), rows, E, N, K, dt,
@@ -583,9 +592,9 @@ def moe_grouped_ffn_mx(codes, scales, offsets, blobs, F, workspace=None, y_perm=
     _sized(fn, "y_perm", y_perm, (rows, d))
     with _on(fn, codes, scales, offsets, blobs, workspace, y_perm, status):
         if workspace is None:
-            workspace = codes.new_empty((lib.moe_ffn_mx_workspace_bytes(rows, F),))
+            workspace = _new(codes, (lib.moe_ffn_mx_workspace_bytes(rows, F),), torch.uint8, stream)
         if y_perm is None:
-            y_perm = codes.new_empty((rows, d), dtype=torch.float16)
+            y_perm = _new(codes, (rows, d), torch.float16, stream)
         _check(fn, lib.moe_grouped_ffn_mx(
             _ptr(codes, torch.uint8, "codes"), _ptr(scales, torch.uint8, "scales"),
             _ptr(offsets, torch.int32, "offsets"), _ptr(blobs, torch.uint8, "blobs"), rows, E, d, F, _ptr(workspace),

@@ -48,7 +48,7 @@ def check(x, w, k, bias=None, rtol=RTOL, **kw):
 @pytest.mark.parametrize("router", range(len(ROUTERS)))
 # one cluster launch (1 to 8 tokens), fp32 logits, tensor-core logits (from 128 tokens)
 @pytest.mark.parametrize("T,d,E,k", [(1, 2048, 64, 8), (8, 1088, 64, 8), (1, 512, 256, 8), (2, 576, 128, 5), (7, 256, 16, 2),
-                                     (9, 2048, 64, 8), (127, 352, 96, 8), (130, 288, 128, 6), (300, 1024, 256, 8),
+                                     (9, 2048, 64, 8), (3, 96, 64, 4), (127, 352, 96, 8), (130, 288, 128, 6), (300, 1024, 256, 8),
                                      (513, 224, 160, 8)])
 def test_choice_and_weights(T, d, E, k, router):
     kw = dict(ROUTERS[router])
@@ -144,6 +144,40 @@ def test_logit_bounds_hold(T, d, E):
         # sums of terms of magnitude about 2^7 that cancel to about 1e-2: relative to the
         # weights, fp32's rounding shows
         check(x, w, 8, rtol=2e-2, **kw)
+
+
+@pytest.mark.parametrize("T", [4, 60, 200])
+def test_subnormal_and_huge_magnitudes(T):
+    """Weights whose lower bf16 parts are subnormal, activations that are, and
+    rows of very large ones."""
+    x, w, b = draw(T, 128, 32, seed=17)
+    scale = torch.exp2(torch.linspace(-120, 120, T)).bfloat16()[:, None]
+    x = x * scale
+    for ws in (2.0 ** -110, 1.0, 2.0 ** 6):
+        for kw in (dict(), dict(scoring="sigmoid", bias=b), dict(scoring="sigmoid", n_groups=4, topk_groups=2)):
+            # logits up to 2^120: where they are far apart in fp32's rounding the softmax's weights show it
+            idx, _ = moeq.moe_route_scored(x.cuda(), (w * ws).cuda(), 4, **{k: v.cuda() if k == "bias" else v for k, v in kw.items()})
+            ref, _, _ = M.route_scored(x.double().numpy(), (w * ws).double().numpy(), 4,
+                                       **{k: v.double().numpy() if k == "bias" else v for k, v in kw.items()})
+            np.testing.assert_array_equal(idx.cpu().numpy(), ref)
+
+
+def test_calls_on_two_streams_at_once():
+    """Two streams, no order between them, workspaces and outputs allocated by
+    the calls: each gives what it gives alone."""
+    args = [tuple(t.cuda() for t in draw(300, 512, 64, seed=20 + i)) for i in range(2)]
+    want = [moeq.moe_route_scored(x, w, 4, bias=b, scoring="sigmoid") for x, w, b in args]
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    for s in streams:
+        s.wait_stream(torch.cuda.current_stream())
+    got = [[], []]
+    for _ in range(20):
+        for i, (x, w, b) in enumerate(args):
+            got[i].append(moeq.moe_route_scored(x, w, 4, bias=b, scoring="sigmoid", stream=streams[i]))
+    torch.cuda.synchronize()
+    for i in range(2):
+        for idx, wt in got[i]:
+            assert torch.equal(idx, want[i][0]) and torch.equal(wt, want[i][1])
 
 
 def test_workspace_of_the_largest_batch_serves_the_smaller():

@@ -21,7 +21,7 @@ def route(L, T=4, d=256, E=64, k=8, scoring=1, groups=8, kept=4, top=2, x=P, w=P
 @pytest.mark.parametrize("args,code,words", [
     (dict(T=-1), INVALID, "bad sizes"), (dict(d=0), INVALID, "bad sizes"), (dict(x=None), INVALID, "null"),
     (dict(idx=None), INVALID, "null"), (dict(k=65), SHAPE, "k <= E"), (dict(k=17), SHAPE, "k <= 16"),
-    (dict(E=512, groups=8), SHAPE, "E <= 256"), (dict(d=250), SHAPE, "multiple of 32"),
+    (dict(E=512, groups=8), SHAPE, "E <= 256"), (dict(d=250), SHAPE, "multiple of 32"), (dict(d=32800), SHAPE, "32768"),
     (dict(scoring=2), INVALID, "scoring"), (dict(groups=0), INVALID, "groups"), (dict(groups=7), INVALID, "groups"),
     (dict(kept=9), INVALID, "groups"), (dict(kept=0), INVALID, "groups"), (dict(top=3), INVALID, "groups"),
     (dict(groups=64, kept=64, top=1), SHAPE, "32 groups"), (dict(groups=8, kept=1, k=9), SHAPE, "k=9"),
