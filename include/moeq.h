@@ -435,8 +435,9 @@ MOE_API moe_status_t moe_mx_pack_ffn(const void* w_gate, const void* w_up, const
  * Products are exact, sums fp32, the result rounded once; rows that belong to
  * no expert keep what they held.  An fp16 output beyond the range flags
  * MOE_DEV_RANGE, offsets outside [0, rows] are clamped and flag
- * MOE_DEV_BAD_INDEX.  Requires N, K multiples of 128, E <= 256 and 16-byte
- * aligned codes, scales, mats and out. */
+ * MOE_DEV_BAD_INDEX.  Requires N, K multiples of 128, E <= 256,
+ * (rows / 128 + 1) * E * ceil(N / 256) < 2^30 and 16-byte aligned codes,
+ * scales, mats and out. */
 MOE_API moe_status_t moe_mx_grouped_gemm(const void* codes, const void* scales, const int32_t* offsets,
                                          const void* mats, int rows, int E, int N, int K, int out_dtype, void* out,
                                          int32_t* status, moe_stream_t stream);

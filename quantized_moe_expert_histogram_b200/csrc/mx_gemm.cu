@@ -35,6 +35,14 @@
 // 64 experts, 1 token 23.8 -> 20.1 us, product of 512 x 4096 x 4096 14.1 ->
 // 13.1 us.
 //
+// What bounds it where experts have many rows: the way from L2 to the SMs.  A
+// stage is 52 KB for 512 cycles of products; 32768 rows of 64 experts, 2048 x
+// 2048 and 2048 x 1024 (an FFN: 160 us, 2.6 PFLOP/s) load and store 1.6 GB
+// through it, 16384 rows of 8 experts at d = 4096, F = 14336 (1.46 ms, 4.0
+// PFLOP/s) 17.5 GB: 10 and 12 TB/s.  Sixteen epilogue warps in place of eight
+// took 182 us for the first; pairs of SMs that share a weight tile (half its
+// bytes) were 5 % faster at 2048 rows an expert and up to 18 % slower below.
+//
 // Every wait is bounded; on a timeout the CTA raises MOE_DEV_TIMEOUT, lets its
 // copies land, frees tensor memory and returns.
 #include <cudaTypedefs.h>
@@ -615,9 +623,10 @@ moe_status_t check(const char* fn, const void* codes, const void* scales, const 
     set_error("%s: N=%d and K=%d must be multiples of 128 (up to 2^24), E=%d at most %d", fn, N, K, E, kMxMaxExperts);
     return MOE_ERR_UNSUPPORTED_SHAPE;
   }
-  // tile numbers and row tiles are 32-bit
-  if ((static_cast<long>(rows) / kM + E) * (N / 64) > 0x7FFFFFFFL) {
-    set_error("%s: rows=%d x N=%d is more than 2^31 - 1 tiles", fn, rows, N);
+  // tile numbers are 32-bit, whatever the offsets hold (out of order, every
+  // expert could claim all the rows)
+  if ((static_cast<long>(rows) / kM + 1) * E * ceil_div(N, kNT) * 2 > 0x7FFFFFFFL) {
+    set_error("%s: rows=%d, E=%d, N=%d could make more than 2^31 - 1 tiles", fn, rows, E, N);
     return MOE_ERR_UNSUPPORTED_SHAPE;
   }
   if (rows == 0) return MOE_OK;

@@ -73,6 +73,8 @@ def ffn(L, rows=8, E=4, d=128, F=128, ws=P, nbytes=1 << 20, codes=P, out=P):
     (dict(K=96), SHAPE, "128"), (dict(E=257), SHAPE, "256"), (dict(dtype=5), INVALID, "dtype"),
     (dict(codes=None), INVALID, "null"), (dict(off=None), INVALID, "null"), (dict(out=P + 2), INVALID, "aligned"),
     (dict(scales=P + 8), INVALID, "aligned"), (dict(rows=2 ** 31 - 1, N=1 << 24), SHAPE, "tiles"),
+    # out of order, the offsets of 256 experts could claim all the rows 128 times
+    (dict(rows=1 << 20, N=1 << 19, E=256), SHAPE, "tiles"),
 ])
 def test_grouped_gemm_refuses(lib, args, code, words):
     assert gemm(lib, **args) == code
