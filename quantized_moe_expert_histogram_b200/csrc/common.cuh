@@ -453,19 +453,15 @@ moe_status_t launch_route(const void* x, const float* w_router, const float* bia
 size_t route_workspace_bytes(int T, int d, int E);
 // fp32 logits of every (token, expert) in slices of d, with the squared
 // norms: logit = sum over s < splits of partial[s][T][E], |error| <= gamma
-// |x| |W_e| (1 + 2^-8) (|x|^2 = sum of xsq[s][T], |W_e|^2 = sum over the
-// first w_splits of wsq[s][E]; the 2^-8 for the norms' own rounding).  The
-// first step of moe_route_scored, on the fp32 pipe (moe_route_topk's first
-// step) or on the tensor cores.
+// |x| |W_e| (1 + 2^-8) (|x|^2 = sum of xsq[s][T], |W_e|^2 = wsq[E]; the 2^-8
+// for the norms' own rounding).  The first step of moe_route_scored.
 struct RoutePartials {
   const float* partial;
   const float* xsq;
   const float* wsq;
-  int splits, w_splits;
+  int splits;
   float gamma;
 };
-moe_status_t launch_route_partials(const void* x, const float* w_router, int T, int d, int E, int k, void* workspace,
-                                   size_t workspace_bytes, RoutePartials* out, cudaStream_t s);
 moe_status_t launch_route_partials_tc(const void* x, const float* w_router, int T, int d, int E, void* workspace,
                                       int32_t* status, RoutePartials* out, cudaStream_t s);
 size_t route_tc_workspace_bytes(int T, int d, int E);

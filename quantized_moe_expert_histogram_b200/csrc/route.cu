@@ -558,16 +558,6 @@ size_t route_min_workspace_bytes(int T, int d, int E) {
   return route_ws_for(1, T, E);
 }
 
-moe_status_t launch_route_partials(const void* x, const float* w_router, int T, int d, int E, int k, void* workspace,
-                                   size_t workspace_bytes, RoutePartials* out, cudaStream_t s) {
-  const int splits = route_splits(T, d, E, workspace_bytes);
-  const RouteWs ws = route_ws(workspace, splits, T, E);
-  *out = {ws.partial, ws.xsq, ws.wsq, splits, splits, 2.0f * route_gamma(d)};
-  const __nv_bfloat16* xb = static_cast<const __nv_bfloat16*>(x);
-  return E <= 16 ? launch_logits<16>(xb, w_router, T, d, E, k, splits, ws, s)
-                 : launch_logits<64>(xb, w_router, T, d, E, k, splits, ws, s);
-}
-
 moe_status_t launch_route(const void* x, const float* w_router, const float* bias,
                           const int32_t* forced, int T, int d, int E, int k, int32_t* idx,
                           float* w, void* workspace, size_t workspace_bytes, cudaStream_t s) {

@@ -26,6 +26,17 @@
 // division (2 ulp) by less than 6 u s, the bias addition by u |c|.
 // Softmax: every numerator and the denominator err by a relative
 // 2 D_max + 4 u (|l - max|) + (E / 32 + 20) u at most, D_max <= 0.05.
+//
+// A warp takes a token, its experts spread over the lanes, so the picks are
+// warp reductions and the intervals stay in registers; what is open goes to
+// the whole CTA, an expert's fp64 dot product to a warp, because the tokens
+// of a CTA have very different numbers of open experts (a warp refining its
+// own token's took 106 us in place of 94 for 8191 tokens, 256 experts, d =
+// 4096).  The time goes into waiting, on those products' barriers and loads
+// (41 % of the issue slots busy): of 91 us for that call the weights' split
+// takes 5, the logits 50 and this kernel the rest.  4096 tokens, 256
+// experts, 4 of 8 groups, d = 2048: 47 us; 250 tokens, 128 experts, d = 4096: 27
+// us.  Up to 8 tokens with few logits run as one launch of a cluster (below).
 #include "common.cuh"
 
 namespace moeq {
@@ -208,16 +219,16 @@ __device__ __noinline__ int pick_whole(const Scored& A, Row<P>& row, int lane, d
 }
 
 // The tokens block * kWarps .. of a CTA, a warp to each; P experts per lane
-// (expert lane + 32 m), R rows in shared memory (the block has no more tokens).
+// (expert lane + 32 m).
 // load(t, L, D): the token's fp32 logits and bounds.
-template <int P, int R = kWarps, typename Load>
+template <int P, typename Load>
 __device__ __forceinline__ void select_block(const Scored& A, Row<P>* rows, int block, Load load) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int T = A.T, E = A.E, k = A.k, G = A.groups, gs = E / G;
   const int t = block * kWarps + warp;
   const bool here = t < T, grouped = A.kept < G;
   const bool alone = A.sigmoid || A.by_logits;  // an expert's choice value needs no other's logit
-  Row<P>& row = rows[min(warp, R - 1)];  // (a warp without a token writes nothing)
+  Row<P>& row = rows[warp];
   float C[P], D[P];
   uint32_t in_range = 0, refined = 0;  // bit m: expert lane + 32 m
   bool hard = false;                   // the whole row goes to fp64
@@ -292,14 +303,14 @@ __device__ __forceinline__ void select_block(const Scored& A, Row<P>* rows, int 
       if ((open >> m) & 1u) row.cand[n + __popc(bal & ((1u << lane) - 1u))] = static_cast<uint8_t>(lane + 32 * m);
       n += __popc(bal);
     }
-    if (lane == 0 && warp < R) {
+    if (lane == 0) {
       row.n = n;
       row.raw = A.by_logits || hard || !alone;
     }
     __syncthreads();
     int total = 0;
 #pragma unroll
-    for (int w = 0; w < R; ++w) total += rows[w].n;
+    for (int w = 0; w < kWarps; ++w) total += rows[w].n;
     for (int item = warp; item < total; item += kWarps) {
       int w = 0, r = item;
       while (r >= rows[w].n) r -= rows[w++].n;
@@ -569,9 +580,9 @@ __global__ void __launch_bounds__(kThreads, 3) k_route_scored(const __grid_const
   pdl_trigger();
   select_block<P>(A, rows, blockIdx.x, [&](int t, float (&L)[P], float (&D)[P]) {
     const int lane = threadIdx.x & 31, T = A.T, E = A.E;
-    float xq = 0.f, wq[P];
+    float xq = 0.f;
 #pragma unroll
-    for (int m = 0; m < P; ++m) L[m] = wq[m] = 0.f;
+    for (int m = 0; m < P; ++m) L[m] = 0.f;
 #pragma unroll 4
     for (int s = 0; s < A.lg.splits; ++s) {
       xq += A.lg.xsq[static_cast<size_t>(s) * T + t];
@@ -580,15 +591,10 @@ __global__ void __launch_bounds__(kThreads, 3) k_route_scored(const __grid_const
       for (int m = 0; m < P; ++m)
         if (lane + 32 * m < E) L[m] += pl[32 * m];
     }
-#pragma unroll 4
-    for (int s = 0; s < A.lg.w_splits; ++s)
-#pragma unroll
-      for (int m = 0; m < P; ++m)
-        if (lane + 32 * m < E) wq[m] += A.lg.wsq[static_cast<size_t>(s) * E + lane + 32 * m];
     const float xn = sqrt_approx(xq);
 #pragma unroll
     for (int m = 0; m < P; ++m) {
-      const float wn = sqrt_approx(wq[m]);
+      const float wn = sqrt_approx(lane + 32 * m < E ? A.lg.wsq[lane + 32 * m] : 0.f);
       D[m] = A.lg.gamma * xn * wn * (1.0f + 0.00390625f) + 1.2e-7f * fabsf(L[m]) + 7e-36f * (xn + wn) + 1e-30f;
     }
   });
@@ -598,13 +604,16 @@ __global__ void __launch_bounds__(kThreads, 3) k_route_scored(const __grid_const
 // cluster.  A CTA sums one slice of d for all T E logits (fp32 FMA chains of
 // the products and of their magnitudes, cluster_partial_dots_f32) into CTA 0,
 // which selects:  |L - l| <= 2 cluster_gamma(d) (sum of magnitudes)(1 + 2^-8).
-constexpr int tiny_logits(int P) { return P <= 2 ? 512 : 256; }  // 48 KB of shared memory
-constexpr int tiny_rows(int P) { return P == 8 ? 1 : kWarps; }   // E > 128: 256 logits are one token's
+// Taken up to 128 logits, where it is the faster (us in a graph, this kernel
+// against the tensor-core logits and k_route_scored): 64 experts, d = 2048: 1
+// token 7.0 / 13.8, 2 tokens 10.1 / 12.7, 4 tokens 16.3 / 16.3, 8 tokens 28.3 /
+// 16.3; 128 experts, d = 4096: 1 token 13.0 / 20.5, 2 tokens 21.2 / 15.4.
+constexpr int kTinyLogits = 128;
 
 template <int P>
 __global__ void __launch_bounds__(kThreads) k_route_scored_tiny(const __grid_constant__ Scored A) {
-  __shared__ Row<P> rows[tiny_rows(P)];
-  __shared__ float2 part[kClusterSlices * tiny_logits(P)];
+  __shared__ Row<P> rows[kWarps];
+  __shared__ float2 part[kClusterSlices * kTinyLogits];
   cluster_sync_start();
   pdl_wait();
   pdl_trigger();
@@ -620,7 +629,7 @@ __global__ void __launch_bounds__(kThreads) k_route_scored_tiny(const __grid_con
       cluster_map_shared(part, 0) + 8u * static_cast<uint32_t>(rank * n));
   cluster_sync_publish();
   if (rank != 0) return;
-  select_block<P, tiny_rows(P)>(A, rows, 0, [&](int t, float (&L)[P], float (&D)[P]) {
+  select_block<P>(A, rows, 0, [&](int t, float (&L)[P], float (&D)[P]) {
     const int lane = threadIdx.x & 31;
 #pragma unroll
     for (int m = 0; m < P; ++m) {
@@ -639,10 +648,7 @@ __global__ void __launch_bounds__(kThreads) k_route_scored_tiny(const __grid_con
   });
 }
 
-bool tiny(int T, int d, int E) { return T <= kWarps && d % 64 == 0 && T * E <= tiny_logits(ceil_div(E, 32)); }
-
-// The logits' kernel: the tensor cores for batches that fill a tile's tokens.
-constexpr int kTensorT = 128;
+bool tiny(int T, int d, int E) { return T <= kWarps && d % 64 == 0 && T * E <= kTinyLogits; }
 
 }  // namespace
 }  // namespace moeq
@@ -653,8 +659,7 @@ extern "C" {
 
 size_t moe_route_scored_workspace_bytes(int T, int d, int E) {
   if (T <= 0 || d <= 0 || E <= 0) return 256;
-  const size_t small = route_workspace_bytes(std::min(T, kTensorT - 1), d, E);
-  return T >= kTensorT ? std::max(small, route_tc_workspace_bytes(T, d, E)) : small;
+  return route_tc_workspace_bytes(T, d, E);
 }
 
 moe_status_t moe_route_scored(const void* x, const float* w_router, const float* bias, int T, int d, int E, int k,
@@ -694,9 +699,7 @@ moe_status_t moe_route_scored(const void* x, const float* w_router, const float*
   }
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   Scored A{};
-  if (!tiny(T, d, E))
-    st = T >= kTensorT ? launch_route_partials_tc(x, w_router, T, d, E, workspace, status, &A.lg, s)
-                          : launch_route_partials(x, w_router, T, d, E, k, workspace, workspace_bytes, &A.lg, s);
+  if (!tiny(T, d, E)) st = launch_route_partials_tc(x, w_router, T, d, E, workspace, status, &A.lg, s);
   if (st != MOE_OK) return st;
   A.x = static_cast<const __nv_bfloat16*>(x);
   A.w = w_router;
@@ -716,10 +719,7 @@ moe_status_t moe_route_scored(const void* x, const float* w_router, const float*
   A.out_w = topk_w;
   if (tiny(T, d, E)) {
     A.lg.gamma = cluster_gamma(d);
-    auto kern = E <= 32   ? k_route_scored_tiny<1>
-                : E <= 64 ? k_route_scored_tiny<2>
-                : E <= 128 ? k_route_scored_tiny<4>
-                           : k_route_scored_tiny<8>;
+    auto kern = E <= 32 ? k_route_scored_tiny<1> : E <= 64 ? k_route_scored_tiny<2> : k_route_scored_tiny<4>;
     return cuda_check(launch_cluster_pdl(kern, kClusterSlices, dim3(kThreads), 0, s, A), "moe_route_scored launch");
   }
   auto kern = E <= 32 ? k_route_scored<1> : E <= 64 ? k_route_scored<2> : E <= 128 ? k_route_scored<4> : k_route_scored<8>;

@@ -46,7 +46,7 @@ def check(x, w, k, bias=None, rtol=RTOL, **kw):
 
 
 @pytest.mark.parametrize("router", range(len(ROUTERS)))
-# one cluster launch (1 to 8 tokens), fp32 logits, tensor-core logits (from 128 tokens)
+# one cluster launch (up to 8 tokens and 128 logits), tensor-core logits otherwise
 @pytest.mark.parametrize("T,d,E,k", [(1, 2048, 64, 8), (8, 1088, 64, 8), (1, 512, 256, 8), (2, 576, 128, 5), (7, 256, 16, 2),
                                      (9, 2048, 64, 8), (3, 96, 64, 4), (127, 352, 96, 8), (130, 288, 128, 6), (300, 1024, 256, 8),
                                      (513, 224, 160, 8)])
