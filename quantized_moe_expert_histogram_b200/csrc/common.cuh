@@ -461,6 +461,12 @@ struct RoutePartials {
   const float* wsq;
   int splits;
   float gamma;
+  // for the tokens that need fp64 logits of every expert: list[0] of them
+  // (cleared), list[1 ..] their indices, and `room` bytes for those logits,
+  // at least 8 T E; they overlie partial
+  int32_t* list;
+  double* rows64;
+  size_t room;
 };
 moe_status_t launch_route_partials_tc(const void* x, const float* w_router, int T, int d, int E, void* workspace,
                                       int32_t* status, RoutePartials* out, cudaStream_t s);

@@ -53,6 +53,8 @@ struct Scored {
   int T, d, E, k;
   int sigmoid, groups, kept, group_top, renorm;
   int by_logits;  // c rises with l: compare the logits
+  int alone;      // an expert's choice value needs no other's logit
+  int32_t* list;  // where not: the tokens left for k_route_rows64 and k_route_whole (null: done here)
   float scale;
   int32_t* out_idx;
   float* out_w;
@@ -66,6 +68,7 @@ struct Row {
   uint8_t cand[32 * P];                   // experts to refine; later the experts left out that may come in
   int n;
   int raw;  // v holds logits
+  float shift;  // softmax without a bias: values are e^(l - shift)
 };
 
 // 2^-23 relative (the bounds have 2^-8 to spare for the norms).
@@ -218,6 +221,17 @@ __device__ __noinline__ int pick_whole(const Scored& A, Row<P>& row, int lane, d
   return mine;
 }
 
+// The weight of lane j's pick (j < k) from its fp64 score.
+__device__ __forceinline__ float weight64(const Scored& A, double s, int lane) {
+  if (A.renorm) {
+    double sum = lane < A.k ? s : 0.0;
+#pragma unroll
+    for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    s = sum == 0.0 ? 0.0 : s / sum;
+  }
+  return static_cast<float>(s * A.scale);
+}
+
 // The tokens block * kWarps .. of a CTA, a warp to each; P experts per lane
 // (expert lane + 32 m).
 // load(t, L, D): the token's fp32 logits and bounds.
@@ -227,7 +241,7 @@ __device__ __forceinline__ void select_block(const Scored& A, Row<P>* rows, int 
   const int T = A.T, E = A.E, k = A.k, G = A.groups, gs = E / G;
   const int t = block * kWarps + warp;
   const bool here = t < T, grouped = A.kept < G;
-  const bool alone = A.sigmoid || A.by_logits;  // an expert's choice value needs no other's logit
+  const bool alone = A.alone;
   Row<P>& row = rows[warp];
   float C[P], D[P];
   uint32_t in_range = 0, refined = 0;  // bit m: expert lane + 32 m
@@ -265,6 +279,7 @@ __device__ __forceinline__ void select_block(const Scored& A, Row<P>* rows, int 
       for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
       row_max = mx;
       row_sum = sum;
+      if (lane == 0) row.shift = mx;
     }
     bool wide = false;
 #pragma unroll
@@ -277,6 +292,9 @@ __device__ __forceinline__ void select_block(const Scored& A, Row<P>* rows, int 
         if (A.sigmoid) {
           s = __fdividef(1.0f, 1.0f + __expf(-L[m]));
           ds = (1.06f * D[m] + 1.2e-7f * (2.0f + 1.2f * fabsf(L[m]))) * (s * (1.0f - s) + 2.0e-7f) + 4.0e-7f * s;
+        } else if (!A.bias) {
+          s = expf(L[m] - row_max);
+          ds = s * (1.06f * D[m] + 2.4e-7f * (row_max - L[m]) + 6e-7f);
         } else {
           s = __fdividef(expf(L[m] - row_max), row_sum);
           ds = s * (2.2f * d_max + 2.4e-7f * (row_max - L[m]) + 6.0e-8f * (E / 32 + 20)) * 1.06f;
@@ -316,7 +334,9 @@ __device__ __forceinline__ void select_block(const Scored& A, Row<P>* rows, int 
       while (r >= rows[w].n) r -= rows[w++].n;
       const int tu = block * kWarps + w, e = rows[w].cand[r];
       double v = dot_bf16_f32_fp64(A.x + static_cast<size_t>(tu) * A.d, A.w + static_cast<size_t>(e) * A.d, A.d, lane);
-      if (!rows[w].raw) v = ordered(1.0 / (1.0 + exp(-v)) + (A.bias ? static_cast<double>(A.bias[e]) : 0.0));
+      if (!rows[w].raw)
+        v = A.sigmoid ? ordered(1.0 / (1.0 + exp(-v)) + (A.bias ? static_cast<double>(A.bias[e]) : 0.0))
+                      : exp(v - static_cast<double>(rows[w].shift));
       if (lane == 0) rows[w].v[e] = v;
     }
     __syncthreads();
@@ -378,7 +398,8 @@ __device__ __forceinline__ void select_block(const Scored& A, Row<P>* rows, int 
     }
   }
   if (!here) hard = false;
-  if (hard) open = in_range;
+  bool listed = hard && A.list;
+  if (hard) open = listed ? 0 : in_range;
   refine(open);
   if (here && group_open && !hard) {
     // the open groups by their fp64 scores: d = -1 marks the experts refined,
@@ -459,7 +480,8 @@ __device__ __forceinline__ void select_block(const Scored& A, Row<P>* rows, int 
     const float lo_last = __shfl_sync(0xffffffffu, lo, k - 1);
     again = __any_sync(0xffffffffu, (out && hi >= lo_last) || (lane > 0 && lane < k && !(lo_prev > up)));
     if (again && !alone) {
-      open = in_range;
+      listed = A.list;
+      open = listed ? 0 : in_range;
     } else if (again) {
       float lo_min = lo;
 #pragma unroll
@@ -490,6 +512,11 @@ __device__ __forceinline__ void select_block(const Scored& A, Row<P>* rows, int 
   }
   refine(open);
   if (!here) return;
+  if (listed) {
+    // (the order of the list changes from run to run; nothing depends on it)
+    if (lane == 0) A.list[1 + atomicAdd(A.list, 1)] = t;
+    return;
+  }
   __syncwarp();
   double s64 = 0.0;
   const bool whole = hard || (again && !alone);
@@ -542,13 +569,7 @@ __device__ __forceinline__ void select_block(const Scored& A, Row<P>* rows, int 
   // ---- weights: lane j < k holds pick j ----------------------------------------------
   float wt;
   if (whole) {
-    if (A.renorm) {
-      double sum = lane < k ? s64 : 0.0;
-#pragma unroll
-      for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-      s64 = sum == 0.0 ? 0.0 : s64 / sum;
-    }
-    wt = static_cast<float>(s64 * A.scale);
+    wt = weight64(A, s64, lane);
   } else {
     const float l = row.l[mine];
     float s = A.sigmoid ? 1.0f / (1.0f + expf(-l)) : expf(l - row_max);
@@ -598,6 +619,128 @@ __global__ void __launch_bounds__(kThreads, 3) k_route_scored(const __grid_const
       D[m] = A.lg.gamma * xn * wn * (1.0f + 0.00390625f) + 1.2e-7f * fabsf(L[m]) + 7e-36f * (xn + wn) + 1e-30f;
     }
   });
+}
+
+// Tokens whose choice a softmax's denominator leaves open: fp64 logits of all
+// their experts, as a product of tiles (a weight row read by one token at a
+// time would cost 16 E d / 4 bytes a token: 4 MB and 40 us a CTA at 256 experts,
+// d = 4096).  Tile: 32 listed tokens x 64 experts over a slice of d, a thread 4
+// x 2; operands are converted once, on their way into shared memory.  Few
+// tokens: d is cut into slices while SMs are idle and there is room; their
+// sums are added in order.
+constexpr int kRT = 32, kRE = 64, kRK = 32;
+
+struct Slices {
+  int count, tiles_t, tiles_e, slices, per;  // per: chunks of kRK
+};
+__device__ __forceinline__ Slices slices_of(const int32_t* list, size_t room, int T, int E, int d) {
+  Slices S;
+  S.count = min(list[0], T);
+  S.tiles_t = (S.count + kRT - 1) / kRT;
+  S.tiles_e = (E + kRE - 1) / kRE;
+  const int chunks = d / kRK, tiles = max(1, S.tiles_t * S.tiles_e);
+  const size_t fit = room / (static_cast<size_t>(max(S.count, 1)) * E * 8);
+  const int want = static_cast<int>(min(fit, static_cast<size_t>(max(1, 296 / tiles))));
+  S.per = (chunks + min(want, chunks) - 1) / min(want, chunks);
+  S.slices = (chunks + S.per - 1) / S.per;
+  return S;
+}
+
+__global__ void __launch_bounds__(256) k_route_rows64(const __nv_bfloat16* __restrict__ x, const float* __restrict__ w,
+                                                      const int32_t* list, size_t room, int T, int E, int d,
+                                                      double* out) {
+  __shared__ __align__(16) double xs[kRK][kRT], ws[kRK][kRE];
+  pdl_wait();
+  pdl_trigger();
+  const Slices S = slices_of(list, room, T, E, d);
+  const int tid = threadIdx.x, chunks = d / kRK;
+  const int tx = (tid & 7) * 4, te = (tid >> 3) * 2;  // the thread's tokens, experts
+  const int units = S.tiles_t * S.tiles_e * S.slices;
+  for (int u = blockIdx.x; u < units; u += gridDim.x) {
+    const int sl = u % S.slices, tile = u / S.slices;
+    const int i0 = tile / S.tiles_e * kRT, e0 = tile % S.tiles_e * kRE;
+    const int c0 = sl * S.per, c1 = min(chunks, c0 + S.per);
+    // loads: 8 elements of a token (threads below 128), two pieces of 4 of an expert
+    const int lt = tid & 31, lk = (tid >> 5) * 8;
+    const bool has_x = tid < 128 && i0 + lt < S.count;
+    const __nv_bfloat16* xp = x + (has_x ? static_cast<size_t>(min(max(list[1 + i0 + lt], 0), T - 1)) * d + lk : 0);
+    const int le = tid & 63, lj = (tid >> 6) * 4;
+    const bool has_w = e0 + le < E;
+    const float* wp = w + (has_w ? static_cast<size_t>(e0 + le) * d + lj : 0);
+    uint4 xv = make_uint4(0, 0, 0, 0);
+    float4 w0 = make_float4(0, 0, 0, 0), w1 = w0;
+    auto load = [&](int c) {
+      if (has_x) xv = *reinterpret_cast<const uint4*>(xp + c * kRK);
+      if (has_w) {
+        w0 = *reinterpret_cast<const float4*>(wp + c * kRK);
+        w1 = *reinterpret_cast<const float4*>(wp + c * kRK + 16);
+      }
+    };
+    double a[4][2];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) a[i][0] = a[i][1] = 0.0;
+    load(c0);
+    for (int c = c0; c < c1; ++c) {
+      __syncthreads();  // the chunk before has been read
+      if (tid < 128) {
+        const uint32_t q[4] = {xv.x, xv.y, xv.z, xv.w};
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          xs[lk + 2 * j][lt] = static_cast<double>(__uint_as_float(q[j] << 16));
+          xs[lk + 2 * j + 1][lt] = static_cast<double>(__uint_as_float(q[j] & 0xFFFF0000u));
+        }
+      }
+      ws[lj][le] = w0.x; ws[lj + 1][le] = w0.y; ws[lj + 2][le] = w0.z; ws[lj + 3][le] = w0.w;
+      ws[lj + 16][le] = w1.x; ws[lj + 17][le] = w1.y; ws[lj + 18][le] = w1.z; ws[lj + 19][le] = w1.w;
+      __syncthreads();
+      if (c + 1 < c1) load(c + 1);
+#pragma unroll 8
+      for (int k = 0; k < kRK; ++k) {
+        const double2 p = *reinterpret_cast<const double2*>(&xs[k][tx]), q = *reinterpret_cast<const double2*>(&xs[k][tx + 2]);
+        const double2 v = *reinterpret_cast<const double2*>(&ws[k][te]);
+        const double xk[4] = {p.x, p.y, q.x, q.y};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          a[i][0] = fma(xk[i], v.x, a[i][0]);
+          a[i][1] = fma(xk[i], v.y, a[i][1]);
+        }
+      }
+    }
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+      for (int j = 0; j < 2; ++j)
+        if (i0 + tx + i < S.count && e0 + te + j < E)
+          out[(static_cast<size_t>(sl) * S.count + i0 + tx + i) * E + e0 + te + j] = a[i][j];
+  }
+}
+
+// Picks and weights of the listed tokens, a warp to each.
+template <int P>
+__global__ void __launch_bounds__(kThreads) k_route_whole(const __grid_constant__ Scored A) {
+  __shared__ Row<P> rows[kWarps];
+  pdl_wait();
+  pdl_trigger();
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const Slices S = slices_of(A.list, A.lg.room, A.T, A.E, A.d);
+  for (int i = blockIdx.x * kWarps + warp; i < S.count; i += gridDim.x * kWarps) {
+    const size_t t = min(max(A.list[1 + i], 0), A.T - 1);
+    for (int e = lane; e < A.E; e += 32) {
+      double v = 0.0;
+      for (int s = 0; s < S.slices; ++s) v += A.lg.rows64[(static_cast<size_t>(s) * S.count + i) * A.E + e];
+      rows[warp].v[e] = v;
+    }
+    __syncwarp();
+    double s = 0.0;
+    const int mine = pick_whole<P>(A, rows[warp], lane, s);
+    const float wt = weight64(A, s, lane);
+    if (lane < A.k) {
+      A.out_idx[t * A.k + lane] = mine;
+      A.out_w[t * A.k + lane] = wt;
+    }
+    __syncwarp();
+  }
 }
 
 // The smallest batches: logits and selection in one launch of a thread-block
@@ -714,6 +857,7 @@ moe_status_t moe_route_scored(const void* x, const float* w_router, const float*
   A.group_top = group_top;
   A.renorm = renorm != 0;
   A.by_logits = !bias && (group_top == 1 || topk_groups == n_groups);
+  A.alone = A.sigmoid || !bias;
   A.scale = static_cast<float>(scale);
   A.out_idx = topk_idx;
   A.out_w = topk_w;
@@ -723,8 +867,18 @@ moe_status_t moe_route_scored(const void* x, const float* w_router, const float*
     return cuda_check(launch_cluster_pdl(kern, kClusterSlices, dim3(kThreads), 0, s, A), "moe_route_scored launch");
   }
   auto kern = E <= 32 ? k_route_scored<1> : E <= 64 ? k_route_scored<2> : E <= 128 ? k_route_scored<4> : k_route_scored<8>;
-  return cuda_check(launch_pdl(pdl_for(static_cast<long>(T) * k), kern, dim3(ceil_div(T, kWarps)), dim3(kThreads), 0, s, A),
-                    "moe_route_scored launch");
+  if (!A.alone) A.list = A.lg.list;
+  const bool pdl = pdl_for(static_cast<long>(T) * k);
+  st = cuda_check(launch_pdl(pdl, kern, dim3(ceil_div(T, kWarps)), dim3(kThreads), 0, s, A), "moe_route_scored launch");
+  if (st != MOE_OK || A.alone) return st;
+  st = cuda_check(launch_pdl(true, k_route_rows64, dim3(std::min<long>(296, ceil_div(T, kRT) * 16L * ceil_div(E, kRE))),
+                             dim3(256), 0, s, A.x, A.w, static_cast<const int32_t*>(A.list), A.lg.room, T, E, d,
+                             A.lg.rows64),
+                  "moe_route_scored fp64 launch");
+  if (st != MOE_OK) return st;
+  auto fin = E <= 32 ? k_route_whole<1> : E <= 64 ? k_route_whole<2> : E <= 128 ? k_route_whole<4> : k_route_whole<8>;
+  return cuda_check(launch_pdl(true, fin, dim3(std::min(296, ceil_div(T, kWarps))), dim3(kThreads), 0, s, A),
+                    "moe_route_scored selection launch");
 }
 
 }  // extern "C"

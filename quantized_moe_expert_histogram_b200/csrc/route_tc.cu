@@ -82,10 +82,12 @@ __device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
 
 // W_r row -> its three parts, and its sum of squares.  A CTA per expert.
 __global__ void __launch_bounds__(256) k_route_split(const float* __restrict__ w, int E, int d,
-                                                     __nv_bfloat16* __restrict__ parts, float* __restrict__ wsq) {
+                                                     __nv_bfloat16* __restrict__ parts, float* __restrict__ wsq,
+                                                     int32_t* __restrict__ list) {
   pdl_wait();
   pdl_trigger();
   const int e = blockIdx.x;
+  if (e == 0 && threadIdx.x == 0) list[0] = 0;
   const size_t plane = static_cast<size_t>(E) * d;
   float sq = 0.f;
   for (int i = threadIdx.x * 4; i < d; i += 1024) {
@@ -300,7 +302,7 @@ bool encode(CUtensorMap* m, int rank, const void* base, const cuuint64_t* dims, 
 
 struct Plan {
   int splits, per_split, chunks;
-  size_t xsq, wsq, parts, bytes;  // offsets in the workspace
+  size_t xsq, wsq, list, parts, bytes;  // offsets in the workspace
 };
 
 Plan plan_for(int T, int d, int E) {
@@ -311,9 +313,10 @@ Plan plan_for(int T, int d, int E) {
   p.per_split = ceil_div(p.chunks, want);
   p.splits = ceil_div(p.chunks, p.per_split);
   auto up = [](size_t n) { return (n + 255) / 256 * 256; };
-  p.xsq = up(static_cast<size_t>(p.splits) * T * E * 4);
+  p.xsq = up(static_cast<size_t>(std::max(p.splits, 2)) * T * E * 4);  // (two: one fp64 logit each)
   p.wsq = p.xsq + up(static_cast<size_t>(p.splits) * T * 4);
-  p.parts = p.wsq + up(static_cast<size_t>(E) * 4);
+  p.list = p.wsq + up(static_cast<size_t>(E) * 4);
+  p.parts = p.list + up((static_cast<size_t>(T) + 1) * 4);
   p.bytes = p.parts + static_cast<size_t>(3) * E * d * 2;
   return p;
 }
@@ -362,7 +365,8 @@ moe_status_t launch_route_partials_tc(const void* x, const float* w_router, int 
     if (e != cudaSuccess) return cuda_check(e, "moe_route_scored shared-memory attribute");
     attr_set.fetch_or(bit);
   }
-  moe_status_t st = cuda_check(launch_pdl(false, k_route_split, dim3(E), dim3(256), 0, s, w_router, E, d, parts, wsq),
+  moe_status_t st = cuda_check(launch_pdl(false, k_route_split, dim3(E), dim3(256), 0, s, w_router, E, d, parts, wsq,
+                                          reinterpret_cast<int32_t*>(ws + p.list)),
                                "moe_route_scored split launch");
   if (st != MOE_OK) return st;
   st = cuda_check(launch_pdl(true, k_route_tc, dim3(ceil_div(T, kT), ceil_div(E, kE), p.splits), dim3(kThreads), kSmem,
@@ -370,7 +374,8 @@ moe_status_t launch_route_partials_tc(const void* x, const float* w_router, int 
                   "moe_route_scored logits launch");
   const double u = 1.0 / 16777216.0;
   const double g = 64 * 2 * u + (p.chunks + p.splits + 2) * u + 2.0 * d * 2 * u / 512 * 1.01 + u / 4;
-  *out = {P.partial, P.xsq, wsq, p.splits, static_cast<float>(1.1 * g)};
+  *out = {P.partial, P.xsq, wsq, p.splits, static_cast<float>(1.1 * g), reinterpret_cast<int32_t*>(ws + p.list),
+          reinterpret_cast<double*>(ws), p.xsq};
   return st;
 }
 

@@ -270,3 +270,20 @@ def test_layer_in_a_graph_and_on_another_stream():
     assert torch.equal(got, layer.forward(x2))
     with pytest.raises(ValueError):
         layer.forward(torch.zeros(28, 256, dtype=torch.bfloat16, device="cuda"))
+
+
+@pytest.mark.parametrize("T,d,E", [(9, 4096, 200), (33, 96, 256), (700, 256, 256), (1500, 64, 72)])
+@pytest.mark.parametrize("open_tokens", ["all", "some"])
+def test_softmax_with_bias_by_fp64_rows(T, d, E, open_tokens):
+    """Tokens whose choice hangs on the softmax's denominator: all of them
+    (every expert twice), or those whose two best lie nearly together."""
+    x, w, b = draw(T, d, E, seed=31, std=0.5 / d ** 0.5)
+    if open_tokens == "all":
+        w[E // 2:], b[E // 2:] = w[:E // 2], b[:E // 2]
+    else:
+        b *= 1e-3
+    check(x, w, 7, bias=b)
+    check(x, w, 7, bias=b, n_groups=4, topk_groups=2, group_top=2, renorm=False)
+    a = moeq.moe_route_scored(x.cuda(), w.cuda(), 7, bias=b.cuda())
+    c = moeq.moe_route_scored(x.cuda(), w.cuda(), 7, bias=b.cuda())
+    assert all(torch.equal(p, q) for p, q in zip(a, c))
