@@ -145,7 +145,7 @@ __device__ __forceinline__ void softmax64(const double* v, int E, int lane, doub
   for (int o = 16; o; o >>= 1) mx = fmax(mx, __shfl_xor_sync(0xffffffffu, mx, o));
   if (__any_sync(0xffffffffu, nan)) mx = NAN;
   sum = 0.0;
-#pragma unroll 1
+#pragma unroll 2
   for (int e = lane; e < E; e += 32) sum += exp(v[e] - mx);
 #pragma unroll
   for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
@@ -624,10 +624,12 @@ __global__ void __launch_bounds__(kThreads, 3) k_route_scored(const __grid_const
 // Tokens whose choice a softmax's denominator leaves open: fp64 logits of all
 // their experts, as a product of tiles (a weight row read by one token at a
 // time would cost 16 E d / 4 bytes a token: 4 MB and 40 us a CTA at 256 experts,
-// d = 4096).  Tile: 32 listed tokens x 64 experts over a slice of d, a thread 4
-// x 2; operands are converted once, on their way into shared memory.  Few
-// tokens: d is cut into slices while SMs are idle and there is room; their
-// sums are added in order.
+// d = 4096).  Tile: 32 listed tokens x 64 experts over a slice of d; 64 threads
+// of 8 x 4 sums share a chunk of 32 with three more such groups, each with a
+// quarter of its k (at 4 x 2 sums a thread the loads from shared memory took
+// five times as long as the products).  Few tokens: d is cut into slices
+// while SMs are idle and there is room.  Slices' and groups' sums are added in
+// order.
 constexpr int kRT = 32, kRE = 64, kRK = 32;
 
 struct Slices {
@@ -640,21 +642,22 @@ __device__ __forceinline__ Slices slices_of(const int32_t* list, size_t room, in
   S.tiles_e = (E + kRE - 1) / kRE;
   const int chunks = d / kRK, tiles = max(1, S.tiles_t * S.tiles_e);
   const size_t fit = room / (static_cast<size_t>(max(S.count, 1)) * E * 8);
-  const int want = static_cast<int>(min(fit, static_cast<size_t>(max(1, 296 / tiles))));
+  const int want = static_cast<int>(min(fit, static_cast<size_t>(min(max(1, 296 / tiles), 16))));
   S.per = (chunks + min(want, chunks) - 1) / min(want, chunks);
   S.slices = (chunks + S.per - 1) / S.per;
   return S;
 }
 
-__global__ void __launch_bounds__(256) k_route_rows64(const __nv_bfloat16* __restrict__ x, const float* __restrict__ w,
+__global__ void __launch_bounds__(256, 2) k_route_rows64(const __nv_bfloat16* __restrict__ x, const float* __restrict__ w,
                                                       const int32_t* list, size_t room, int T, int E, int d,
                                                       double* out) {
-  __shared__ __align__(16) double xs[kRK][kRT], ws[kRK][kRE];
+  __shared__ __align__(16) float xs[kRK][kRT], ws[kRK][kRE];
+  __shared__ double red[32 * 64];  // a group's sums
   pdl_wait();
   pdl_trigger();
   const Slices S = slices_of(list, room, T, E, d);
   const int tid = threadIdx.x, chunks = d / kRK;
-  const int tx = (tid & 7) * 4, te = (tid >> 3) * 2;  // the thread's tokens, experts
+  const int group = tid >> 6, tx = (tid & 3) * 8, te = ((tid & 63) >> 2) * 4;  // the thread's k, tokens, experts
   const int units = S.tiles_t * S.tiles_e * S.slices;
   for (int u = blockIdx.x; u < units; u += gridDim.x) {
     const int sl = u % S.slices, tile = u / S.slices;
@@ -676,9 +679,11 @@ __global__ void __launch_bounds__(256) k_route_rows64(const __nv_bfloat16* __res
         w1 = *reinterpret_cast<const float4*>(wp + c * kRK + 16);
       }
     };
-    double a[4][2];
+    double a[8][4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) a[i][0] = a[i][1] = 0.0;
+    for (int i = 0; i < 8; ++i)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) a[i][j] = 0.0;
     load(c0);
     for (int c = c0; c < c1; ++c) {
       __syncthreads();  // the chunk before has been read
@@ -686,33 +691,42 @@ __global__ void __launch_bounds__(256) k_route_rows64(const __nv_bfloat16* __res
         const uint32_t q[4] = {xv.x, xv.y, xv.z, xv.w};
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-          xs[lk + 2 * j][lt] = static_cast<double>(__uint_as_float(q[j] << 16));
-          xs[lk + 2 * j + 1][lt] = static_cast<double>(__uint_as_float(q[j] & 0xFFFF0000u));
+          xs[lk + 2 * j][lt] = __uint_as_float(q[j] << 16);
+          xs[lk + 2 * j + 1][lt] = __uint_as_float(q[j] & 0xFFFF0000u);
         }
       }
       ws[lj][le] = w0.x; ws[lj + 1][le] = w0.y; ws[lj + 2][le] = w0.z; ws[lj + 3][le] = w0.w;
       ws[lj + 16][le] = w1.x; ws[lj + 17][le] = w1.y; ws[lj + 18][le] = w1.z; ws[lj + 19][le] = w1.w;
       __syncthreads();
       if (c + 1 < c1) load(c + 1);
-#pragma unroll 8
-      for (int k = 0; k < kRK; ++k) {
-        const double2 p = *reinterpret_cast<const double2*>(&xs[k][tx]), q = *reinterpret_cast<const double2*>(&xs[k][tx + 2]);
-        const double2 v = *reinterpret_cast<const double2*>(&ws[k][te]);
-        const double xk[4] = {p.x, p.y, q.x, q.y};
+#pragma unroll 2
+      for (int k = group * (kRK / 4); k < (group + 1) * (kRK / 4); ++k) {
+        const float4 p = *reinterpret_cast<const float4*>(&xs[k][tx]), q = *reinterpret_cast<const float4*>(&xs[k][tx + 4]);
+        const float4 v = *reinterpret_cast<const float4*>(&ws[k][te]);
+        const double xk[8] = {p.x, p.y, p.z, p.w, q.x, q.y, q.z, q.w}, wk[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          a[i][0] = fma(xk[i], v.x, a[i][0]);
-          a[i][1] = fma(xk[i], v.y, a[i][1]);
-        }
+        for (int i = 0; i < 8; ++i)
+#pragma unroll
+          for (int j = 0; j < 4; ++j) a[i][j] = fma(xk[i], wk[j], a[i][j]);
       }
     }
-    __syncthreads();
+    for (int g = 1; g < 4; ++g) {
+      __syncthreads();
+      if (group == g)
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
+        for (int r = 0; r < 32; ++r) red[r * 64 + (tid & 63)] = a[r >> 2][r & 3];
+      __syncthreads();
+      if (group == 0)
 #pragma unroll
-      for (int j = 0; j < 2; ++j)
-        if (i0 + tx + i < S.count && e0 + te + j < E)
-          out[(static_cast<size_t>(sl) * S.count + i0 + tx + i) * E + e0 + te + j] = a[i][j];
+        for (int r = 0; r < 32; ++r) a[r >> 2][r & 3] += red[r * 64 + tid];
+    }
+    if (group == 0)
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          if (i0 + tx + i < S.count && e0 + te + j < E)
+            out[(static_cast<size_t>(sl) * S.count + i0 + tx + i) * E + e0 + te + j] = a[i][j];
   }
 }
 
@@ -726,11 +740,18 @@ __global__ void __launch_bounds__(kThreads) k_route_whole(const __grid_constant_
   const Slices S = slices_of(A.list, A.lg.room, A.T, A.E, A.d);
   for (int i = blockIdx.x * kWarps + warp; i < S.count; i += gridDim.x * kWarps) {
     const size_t t = min(max(A.list[1 + i], 0), A.T - 1);
-    for (int e = lane; e < A.E; e += 32) {
-      double v = 0.0;
-      for (int s = 0; s < S.slices; ++s) v += A.lg.rows64[(static_cast<size_t>(s) * S.count + i) * A.E + e];
-      rows[warp].v[e] = v;
+    double v[P];
+#pragma unroll
+    for (int m = 0; m < P; ++m) v[m] = 0.0;
+#pragma unroll 2
+    for (int s = 0; s < S.slices; ++s) {
+      const double* r = A.lg.rows64 + (static_cast<size_t>(s) * S.count + i) * A.E + lane;
+#pragma unroll
+      for (int m = 0; m < P; ++m)
+        if (lane + 32 * m < A.E) v[m] += r[32 * m];
     }
+#pragma unroll
+    for (int m = 0; m < P; ++m) rows[warp].v[lane + 32 * m] = v[m];
     __syncwarp();
     double s = 0.0;
     const int mine = pick_whole<P>(A, rows[warp], lane, s);
