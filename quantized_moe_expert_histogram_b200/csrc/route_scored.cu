@@ -22,7 +22,7 @@
 // open token is evaluated whole: such tokens are listed, and two more
 // kernels compute their logits in fp64 as one product (k_route_rows64) and
 // pick (k_route_whole).  4096 tokens, 256 experts, d = 4096, 330 of them
-// open: 132 us (rows 55, picks 26), 689 when each CTA evaluated its own.
+// open: 128 us (rows 55, picks 25), 689 when each CTA evaluated its own.
 //
 // Carrying the bound (u = 2^-24): sigmoid' = s (1 - s), and over an interval
 // of half width D <= 0.05 it grows by at most e^0.05 < 1.06; __expf errs by (2 +
@@ -632,9 +632,9 @@ __global__ void __launch_bounds__(kThreads, 3) k_route_scored(const __grid_const
 // of 8 x 4 sums share a chunk of 32 with three more such groups, each with a
 // quarter of its k (at 4 x 2 sums a thread, where loads from shared memory
 // took five times as long as the products, 132 us in place of 55 for 330
-// tokens, 256 experts, d = 4096: 6.3 TFLOP/s in fp64, short of the pipe's by
-// the conversions and the chunks' latency; tokens kept as fp64 in shared
-// memory changed nothing).  Few tokens: d is cut into slices
+// tokens, 256 experts, d = 4096: 12.6 TFLOP/s in fp64, short of the pipe's by
+// the conversions; tokens kept as fp64 in shared memory or chunks loaded two
+// ahead changed little, 4 x 4 sums took 66 us).  Few tokens: d is cut into slices
 // while SMs are idle and there is room.  Slices' and groups' sums are added in
 // order.
 constexpr int kRT = 32, kRE = 64, kRK = 32;
@@ -750,7 +750,7 @@ __global__ void __launch_bounds__(kThreads) k_route_whole(const __grid_constant_
     double v[P];
 #pragma unroll
     for (int m = 0; m < P; ++m) v[m] = 0.0;
-#pragma unroll 2
+#pragma unroll (P == 8 ? 4 : 8)
     for (int s = 0; s < S.slices; ++s) {
       const double* r = A.lg.rows64 + (static_cast<size_t>(s) * S.count + i) * A.E + lane;
 #pragma unroll

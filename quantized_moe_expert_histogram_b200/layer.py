@@ -141,15 +141,16 @@ class MxMoELayer:
         T = x.shape[0]
         if T > self.max_tokens:
             raise ValueError(f"T={T} exceeds max_tokens={self.max_tokens}")
-        v = self.views(T)
-        moeq.moe_route_scored(x, self.w_router, self.k, bias=self.bias, topk_idx=v["topk_idx"], topk_w=v["topk_w"],
-                              workspace=v["route_ws"], status=v["status"], stream=stream,
-                              **self.routing)
-        moeq.moe_permute(v["topk_idx"], self.E, out=dict(v, x_perm=None), status=v["status"], workspace=v["perm_ws"],
-                         stream=stream)
-        moeq.moe_mx_quantize(x, inv_perm=v["inv_perm"], k=self.k, codes=v["codes"], scales=v["scales"],
-                             status=v["status"], stream=stream)
-        moeq.moe_grouped_ffn_mx(v["codes"], v["scales"], v["offsets"], self.blobs, self.F, workspace=v["workspace"],
-                                y_perm=v["y_perm"], status=v["status"], stream=stream)
-        return moeq.moe_unpermute_combine(v["y_perm"], v["inv_perm"], v["topk_w"], residual=residual, y=v["y"],
-                                          stream=stream)
+        with moeq._on("MxMoELayer.forward", self.buf["y"], x, residual):
+            v = self.views(T)
+            moeq.moe_route_scored(x, self.w_router, self.k, bias=self.bias, topk_idx=v["topk_idx"], topk_w=v["topk_w"],
+                                  workspace=v["route_ws"], status=v["status"], stream=stream,
+                                  **self.routing)
+            moeq.moe_permute(v["topk_idx"], self.E, out=dict(v, x_perm=None), status=v["status"], workspace=v["perm_ws"],
+                             stream=stream)
+            moeq.moe_mx_quantize(x, inv_perm=v["inv_perm"], k=self.k, codes=v["codes"], scales=v["scales"],
+                                 status=v["status"], stream=stream)
+            moeq.moe_grouped_ffn_mx(v["codes"], v["scales"], v["offsets"], self.blobs, self.F, workspace=v["workspace"],
+                                    y_perm=v["y_perm"], status=v["status"], stream=stream)
+            return moeq.moe_unpermute_combine(v["y_perm"], v["inv_perm"], v["topk_w"], residual=residual, y=v["y"],
+                                              stream=stream)

@@ -287,3 +287,26 @@ def test_softmax_with_bias_by_fp64_rows(T, d, E, open_tokens):
     a = moeq.moe_route_scored(x.cuda(), w.cuda(), 7, bias=b.cuda())
     c = moeq.moe_route_scored(x.cuda(), w.cuda(), 7, bias=b.cuda())
     assert all(torch.equal(p, q) for p, q in zip(a, c))
+
+
+def test_softmax_with_bias_replayed():
+    """The list of open tokens starts anew in every replay."""
+    x, w, b = draw(90, 256, 64, seed=41)
+    w[32:], b[32:] = w[:32], b[:32]             # every token is open
+    xs, wd, bd = x.cuda(), w.cuda(), b.cuda()
+    moeq.moe_route_scored(xs, wd, 4, bias=bd)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        idx, wt = moeq.moe_route_scored(xs, wd, 4, bias=bd)
+    for seed in (42, 43):
+        x = draw(90, 256, 64, seed=seed)[0]
+        xs.copy_(x)
+        g.replay()
+        want = moeq.moe_route_scored(x.cuda(), wd, 4, bias=bd)
+        assert torch.equal(idx, want[0]) and torch.equal(wt, want[1])
+
+
+def test_layer_refuses_tensors_elsewhere():
+    x, wr, b, ws, layer = layer_case(4, 256, 16, 2, 128, 301)
+    with pytest.raises(ValueError, match="MxMoELayer.forward"):
+        layer.forward(x)
