@@ -201,7 +201,9 @@ MOE_API moe_status_t moe_route_topk_noalloc(const void* x, const float* w_router
  *             is that of c in exact arithmetic, evaluated in fp64 where the
  *             fp32 values' error bounds leave it open (without a bias and
  *             with group_top = 1, or without groups, the logits themselves
- *             are compared).
+ *             are compared).  Values that differ by no more than fp64's own
+ *             rounding of a score and a sum (2^-51 for c below 2) may come in
+ *             either order.
  *             A c that is NaN counts as -inf.
  *   topk_w   fp32 [T][k]: s of the picks, divided by the sum over the picks
  *             when renorm != 0 (0 where that sum is 0), times scale; the bias

@@ -453,8 +453,9 @@ moe_status_t launch_route(const void* x, const float* w_router, const float* bia
 size_t route_workspace_bytes(int T, int d, int E);
 // fp32 logits of every (token, expert) in slices of d, with the squared
 // norms: logit = sum over s < splits of partial[s][T][E], |error| <= gamma
-// |x| |W_e| (1 + 2^-8) (|x|^2 = sum of xsq[s][T], |W_e|^2 = wsq[E]; the 2^-8
-// for the norms' own rounding).  The first step of moe_route_scored.
+// |x| |W_e| (1 + 2^-8) (|x|^2 = sum of xsq[s][T] + d 2^-149, |W_e|^2 = wsq[E] +
+// d 2^-149; the 2^-8 for the norms' own rounding, the d 2^-149 for squares
+// below fp32's range).  The first step of moe_route_scored.
 struct RoutePartials {
   const float* partial;
   const float* xsq;

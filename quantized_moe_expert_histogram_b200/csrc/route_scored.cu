@@ -616,10 +616,13 @@ __global__ void __launch_bounds__(kThreads, 3) k_route_scored(const __grid_const
       for (int m = 0; m < P; ++m)
         if (lane + 32 * m < E) L[m] += pl[32 * m];
     }
-    const float xn = sqrt_approx(xq);
+    // What the squares lost below fp32's range: at most 2^-150 each, so d 2^-149
+    // (the subnormal with the bits of d) covers a row of them.
+    const float lost = __uint_as_float(static_cast<uint32_t>(A.d));
+    const float xn = sqrt_approx(xq + lost);
 #pragma unroll
     for (int m = 0; m < P; ++m) {
-      const float wn = sqrt_approx(lane + 32 * m < E ? A.lg.wsq[lane + 32 * m] : 0.f);
+      const float wn = sqrt_approx(lane + 32 * m < E ? A.lg.wsq[lane + 32 * m] + lost : 0.f);
       D[m] = A.lg.gamma * xn * wn * (1.0f + 0.00390625f) + 1.2e-7f * fabsf(L[m]) + 7e-36f * (xn + wn) + 1e-30f;
     }
   });

@@ -17,7 +17,12 @@
 //                         + 2 d 2^-23 2^-9 1.01 + 2^-26)
 // and the select kernel takes 1.1 times that (second-order terms).  Parts and
 // activations that are subnormal in bf16 may count as zero, 2^-126 each: at
-// most 2^-126 sqrt(d) (3 |x| + |W_e|), which the select kernel adds.
+// most 2^-126 sqrt(d) (3 |x| + |W_e|), which the select kernel adds.  Products
+// and sums below fp32's range lose at most 2^-126 each, 12 d of them less than
+// 1e-32: under the 1e-30 that it adds too.  |x| and |W_e| come from fp32 sums of
+// squares, and a square below 2^-150 counts there as zero: the select kernel
+// adds d 2^-149 to each sum (a row of 2^-76 had norm 0 without it, and its
+// near ties were settled on the fp32 sums).
 //
 // A CTA computes 128 experts x 256 tokens of one slice of d: the experts are
 // the M side (a lane of tensor memory is an expert, so a warp's stores of

@@ -1,0 +1,65 @@
+"""The routers where squares, scores or sums leave fp32's range, against the
+fp64 oracle."""
+import numpy as np
+import pytest
+import torch
+
+from oracle import moe_oracle as O
+from oracle import mx_oracle as M
+from quantized_moe_expert_histogram_b200 import build, moeq
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _built():
+    build.build()
+    moeq.load()
+
+
+def swapped_ties(T, d, E, families, seed):
+    """x in steps of 2^-4 and w in steps of 2^-26, so that every fp64 sum is
+    exact in any order while the fp32 sums round; x is the same at 2i and
+    2i + 1, and the rows of a family differ in which of these they swap
+    (equal logits), every fourth of them also by a step in a few places (nearly
+    equal ones)."""
+    g = torch.Generator().manual_seed(seed)
+    x = (torch.randn(T, d // 2, generator=g) * 16).round().clamp(-128, 128) / 16
+    x = x.repeat_interleave(2, 1)
+    base = (torch.randn(families, d // 2, 2, generator=g) * 0.02 * 2 ** 26).round()
+    w = base[torch.arange(E) % families]
+    swap = torch.rand(E, d // 2, generator=g) < 0.5
+    w = torch.where(swap[..., None], w.flip(-1), w)
+    w[torch.arange(E) // families % 4 == 3, ::61, 0] += 1
+    return x, (w / 2 ** 26).reshape(E, d)
+
+
+MAGNITUDES = [(0, 0), (-78, 70), (-78, 0), (-100, 98), (0, -80), (60, -84), (17, -83), (-76, -20)]
+
+
+@pytest.mark.parametrize("T", [4, 60, 300])
+@pytest.mark.parametrize("sx,sw", MAGNITUDES)
+def test_near_ties_at_any_magnitude(sx, sw, T):
+    """Activations of 2^sx and weights of 2^sw: their squares leave fp32's
+    range below, the choice stays that of the fp64 logits."""
+    x, w = swapped_ties(T, 1024, 64, 8, seed=50)
+    x, w = (x * 2.0 ** sx).bfloat16(), w * 2.0 ** sw
+    b = (torch.arange(64) % 8).float() / 1024
+    for kw in (dict(), dict(scoring="sigmoid"), dict(scoring="sigmoid", n_groups=4, topk_groups=2),
+               dict(scoring="sigmoid", bias=b)):
+        idx, _ = moeq.moe_route_scored(x.cuda(), w.cuda(), 12, **{n: v.cuda() if n == "bias" else v for n, v in kw.items()})
+        ref, _, _ = M.route_scored(x.double().numpy(), w.double().numpy(), 12,
+                                   **{n: v.double().numpy() if n == "bias" else v for n, v in kw.items()})
+        got = idx.cpu().numpy()
+        if "bias" not in kw:
+            np.testing.assert_array_equal(got, ref, err_msg=str(kw))
+            continue
+        # Choice values in fp64 are rounded themselves: exp errs by 2^-52 relative at most, 1 + exp, the division and
+        # the bias addition by 2^-53 each, so a value in [0, 2) by less than 2^-52 (exp's error enters s as s (1 - s)
+        # <= 1/4 of it), and two evaluations order values 2^-51 apart alike.  In steps of 2^-110 the logits of a family
+        # differ by about 2^-50, their scores by a quarter of that: the oracle itself differs from an evaluation in 80
+        # bits there.  So: the same picks but for values nearer than 2^-51.
+        l = np.longdouble(x.double().numpy() @ w.double().numpy().T)
+        c = 1 / (1 + np.exp(-l)) + np.longdouble(b.double().numpy())
+        gap = np.abs(np.take_along_axis(c, got.astype(np.int64), 1) - np.take_along_axis(c, ref.astype(np.int64), 1))
+        assert (gap <= 2.0 ** -51).all() and all(len(set(row)) == 12 for row in got.tolist())
