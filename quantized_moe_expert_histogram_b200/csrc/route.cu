@@ -36,7 +36,8 @@
 // g(m) times the sum of their magnitudes; a chunk (32 products) and then the
 // d/32 chunk sums in any order give g(32) + g(d/32)(1 + g(32)) <= g(32 + d/32).
 // The squared norms are fp32 sums too (relative error below 2^-8 for
-// d < 2^15) and the bias addition rounds once more (the u term).
+// d < 2^15; a square below 2^-150 counts as zero, so d 2^-149 is added to
+// each) and the bias addition rounds once more (the u term).
 #include <atomic>
 
 #include "common.cuh"
@@ -346,7 +347,8 @@ __device__ __forceinline__ void select_block(
 #pragma unroll
       for (int u = 0; u < 8; ++u) xq += q[u];
     }
-    const float xn = sqrtf(xq);
+    const float lost = __uint_as_float(static_cast<uint32_t>(d));  // d 2^-149
+    const float xn = sqrtf(xq + lost);
     float* ls = l32[warp];
     float* ds = d32[warp];
 #pragma unroll
@@ -373,7 +375,7 @@ __device__ __forceinline__ void select_block(
         const float b = bias ? bias[e] : 0.f;
         v += b;
         L[m] = v;
-        D[m] = 2.0f * (gamma * xn * sqrtf(wq) * (1.0f + 0.00390625f) +
+        D[m] = 2.0f * (gamma * xn * sqrtf(wq + lost) * (1.0f + 0.00390625f) +
                        5.9604645e-8f * (fabsf(v) + fabsf(b))) + 1e-30f;
         ls[e] = L[m];
         ds[e] = D[m];

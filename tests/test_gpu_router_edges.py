@@ -63,3 +63,13 @@ def test_near_ties_at_any_magnitude(sx, sw, T):
         c = 1 / (1 + np.exp(-l)) + np.longdouble(b.double().numpy())
         gap = np.abs(np.take_along_axis(c, got.astype(np.int64), 1) - np.take_along_axis(c, ref.astype(np.int64), 1))
         assert (gap <= 2.0 ** -51).all() and all(len(set(row)) == 12 for row in got.tolist())
+
+
+@pytest.mark.parametrize("T", [4, 60, 300])
+@pytest.mark.parametrize("sx,sw", MAGNITUDES)
+def test_softmax_router_near_ties_at_any_magnitude(sx, sw, T):
+    x, w = swapped_ties(T, 1024, 64, 8, seed=51)
+    x, w = (x * 2.0 ** sx).bfloat16(), w * 2.0 ** sw
+    idx, _ = moeq.moe_route_topk(x.cuda(), w.cuda(), None, 12)
+    ref = O.topk_select(O.router_logits(x.double().numpy(), w.double().numpy()), 12)
+    np.testing.assert_array_equal(idx.cpu().numpy(), ref)
