@@ -207,7 +207,10 @@ MOE_API moe_status_t moe_route_topk_noalloc(const void* x, const float* w_router
  *             A c that is NaN counts as -inf.
  *   topk_w   fp32 [T][k]: s of the picks, divided by the sum over the picks
  *             when renorm != 0 (0 where that sum is 0), times scale; the bias
- *             does not enter.
+ *             does not enter.  Scores are those that fp64 holds: a sigmoid of a
+ *             logit below -709.78, or a softmax score below e^-745, is 0.  They
+ *             come from the fp32 logits where the choice was settled on those:
+ *             a weight then errs by up to twice the logits' fp32 error.
  *   workspace >= moe_route_scored_workspace_bytes(T, d, E) bytes of device
  *             scratch (enough for any smaller T too), 16-byte aligned (x and
  *             w_router too).

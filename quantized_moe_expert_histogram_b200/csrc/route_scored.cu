@@ -225,6 +225,11 @@ __device__ __noinline__ int pick_whole(const Scored& A, Row<P>& row, int lane, d
   return mine;
 }
 
+// Picks whose largest score is below e^this are weighed in fp64, where scores
+// below e^-709.78 (sigmoid) or e^-745 (softmax) are 0, and so may their sum be.
+// Above it such a score is 0 beside the largest in fp32 too (e^-104 is).
+constexpr float kFarScores = -600.f;
+
 // The weight of lane j's pick (j < k) from its fp64 score.
 __device__ __forceinline__ float weight64(const Scored& A, double s, int lane) {
   if (A.renorm) {
@@ -576,21 +581,30 @@ __device__ __forceinline__ void select_block(const Scored& A, Row<P>* rows, int 
     wt = weight64(A, s64, lane);
   } else {
     const float l = row.l[mine];
-    float s = A.sigmoid ? 1.0f / (1.0f + expf(-l)) : expf(l - row_max);
+    // (sigmoid(l) = e^l (1 + tiny) below -60, and e^-l soon overflows)
+    float s = A.sigmoid ? (l < -60.f ? expf(l) : 1.0f / (1.0f + expf(-l))) : expf(l - row_max), top = 0.f;
     if (A.renorm) {
-      // scores so small that they leave fp32's range: taken from the largest
-      float top = lane < k ? l : -INFINITY;
+      top = lane < k ? l : -INFINITY;
 #pragma unroll
       for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-      if (!A.sigmoid || top < -60.f) s = expf(l - top);  // (sigmoid(l) = e^l (1 + tiny))
-      float sum = lane < k ? s : 0.f;
-#pragma unroll
-      for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-      s /= sum;
-    } else if (!A.sigmoid) {
-      s /= row_sum;
     }
-    wt = s * A.scale;
+    if ((A.sigmoid ? top : top - row_max) < kFarScores && A.renorm) {
+      // scores that leave fp64's range, or nearly: as a row evaluated in fp64 has them
+      wt = weight64(A, A.sigmoid ? 1.0 / (1.0 + exp(-static_cast<double>(l)))
+                                 : exp(static_cast<double>(l) - row_max) / row_sum, lane);
+    } else {
+      if (A.renorm) {
+        // scores so small that they leave fp32's range: taken from the largest
+        if (!A.sigmoid || top < -60.f) s = expf(l - top);
+        float sum = lane < k ? s : 0.f;
+#pragma unroll
+        for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+        s /= sum;
+      } else if (!A.sigmoid) {
+        s /= row_sum;
+      }
+      wt = s * A.scale;
+    }
   }
   if (lane < k) {
     A.out_idx[static_cast<size_t>(t) * k + lane] = mine;

@@ -73,3 +73,32 @@ def test_softmax_router_near_ties_at_any_magnitude(sx, sw, T):
     idx, _ = moeq.moe_route_topk(x.cuda(), w.cuda(), None, 12)
     ref = O.topk_select(O.router_logits(x.double().numpy(), w.double().numpy()), 12)
     np.testing.assert_array_equal(idx.cpu().numpy(), ref)
+
+
+@pytest.mark.parametrize("T", [3, 40])
+@pytest.mark.parametrize("renorm", [True, False])
+@pytest.mark.parametrize("top", [-100.0, -500.0, -599.0, -601.0, -700.0, -709.5, -715.0, -730.0, -760.0])
+def test_weights_of_scores_that_vanish(top, renorm, T):
+    """Scores below fp32's and fp64's range, settled on fp32 logits: the
+    weights are those of the fp64 scores, 0 where their sum is 0.  Logits are
+    sums of two terms that every format here holds exactly; expf, the sum and
+    the division round to less than 1e-6, and near e^-730 the scores themselves
+    are multiples of 2^-1074, 5e-7 of them."""
+    E, k = 32, 6
+    x = torch.zeros(T, 64)
+    x[:, 0], x[:, 1] = 1, torch.arange(T) % 3
+    w = torch.zeros(E, 64)
+    w[:, 0], w[:, 1] = top, -(torch.arange(E) % 16).float() / 4
+    bias = torch.zeros(E)
+    for scoring in ("sigmoid", "softmax"):
+        if scoring == "softmax":    # half of the experts at 0, the bias picks from the other half
+            w[16:, 0], w[16:, 1] = 0, 0
+            bias = torch.where(torch.arange(E) < 16, torch.arange(E) + 2.0, -1.0)
+        args = dict(scoring=scoring, renorm=renorm)
+        idx, wt = moeq.moe_route_scored(x.bfloat16().cuda(), w.cuda(), k, bias=bias.cuda() if scoring == "softmax" else None,
+                                        **args)
+        ref, rw, _ = M.route_scored(x.double().numpy(), w.double().numpy(), k,
+                                    bias=bias.double().numpy() if scoring == "softmax" else None, **args)
+        np.testing.assert_array_equal(idx.cpu().numpy(), ref)
+        # (not renormalised, a score below fp32's range is 0 or subnormal: 2^-149 apart)
+        np.testing.assert_allclose(wt.cpu().numpy(), rw, rtol=1e-5, atol=0 if renorm else 2.0 ** -148)
