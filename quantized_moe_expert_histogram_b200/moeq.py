@@ -5,6 +5,12 @@ nothing but check tensor dtypes/devices, pass raw pointers and sizes, and
 turn a non-zero status into an exception.  All arithmetic runs in the CUDA
 kernels of the library; there is no CPU fallback: ``load()`` raises when
 the library is missing or no CUDA device is present.
+
+``stream=`` (a ``torch.cuda.Stream``; the current one when left out) is where
+a call's kernels run.  Outputs and workspaces that the call makes itself
+belong to that stream, as if made under ``torch.cuda.stream(stream)``; a
+caller who goes on with an output elsewhere makes that stream wait, as for
+any tensor.
 """
 from __future__ import annotations
 
@@ -154,6 +160,28 @@ def _stream(stream):
     return _raw_stream(torch.cuda.current_device())
 
 
+def _new(like, shape, dtype, stream, scratch=False):
+    """A new tensor on the device of `like` for a call on `stream`.
+
+    Its memory comes from the pool of the stream that the call runs on: a
+    block that another stream released may still be read by that stream's
+    queued work.  The tensor returned belongs to that stream; the current
+    stream, on which the caller goes on to use it (after waiting), is recorded
+    as a user, so that the memory is not given out again before it has passed
+    the tensor's release.  scratch: for this call only, dropped before it
+    returns."""
+    if stream is None:
+        return like.new_empty(shape, dtype=dtype)
+    current = torch.cuda.current_stream(like.device)
+    if stream == current:
+        return like.new_empty(shape, dtype=dtype)
+    with torch.cuda.stream(stream):
+        t = like.new_empty(shape, dtype=dtype)
+    if not scratch:
+        t.record_stream(current)
+    return t
+
+
 def moe_blob_bytes(d, F, group, layout):
     return int(load().moe_blob_bytes(d, F, group, layout))
 
@@ -167,7 +195,7 @@ def moe_quant_pack(w_gate, w_up, w_down, group, layout, blobs=None, stream=None)
     E, F, d = w_gate.shape
     nb = lib.moe_blob_bytes(d, F, group, layout)
     if blobs is None:
-        blobs = torch.empty(E, nb, dtype=torch.uint8, device=w_gate.device)
+        blobs = _new(w_gate, (E, nb), torch.uint8, stream)
     _check("moe_quant_pack", lib.moe_quant_pack(
         _ptr(w_gate, torch.float32, "w_gate"), _ptr(w_up, torch.float32, "w_up"),
         _ptr(w_down, torch.float32, "w_down"), E, d, F, group, layout,
@@ -185,11 +213,11 @@ def moe_route_topk(x, w_router, bias, k, forced_idx=None, topk_idx=None, topk_w=
     T, d = x.shape
     E = w_router.shape[0]
     if topk_idx is None:
-        topk_idx = torch.empty(T, k, dtype=torch.int32, device=x.device)
+        topk_idx = _new(x, (T, k), torch.int32, stream)
     if topk_w is None:
-        topk_w = torch.empty(T, k, dtype=torch.float32, device=x.device)
+        topk_w = _new(x, (T, k), torch.float32, stream)
     if workspace is None:
-        workspace = torch.empty(lib.moe_route_workspace_bytes(T, d, E), dtype=torch.uint8, device=x.device)
+        workspace = _new(x, (lib.moe_route_workspace_bytes(T, d, E),), torch.uint8, stream, scratch=True)
     _check("moe_route_topk", lib.moe_route_topk(
         _ptr(x, torch.bfloat16, "x"), _ptr(w_router, torch.float32, "w_router"),
         _ptr(bias, torch.float32, "bias"), _ptr(forced_idx, torch.int32, "forced_idx"), T, d, E, k,
@@ -207,19 +235,18 @@ def moe_permute(topk_idx, E, bits=None, x=None, out=None, status=None, workspace
     lib = load()
     T, k = topk_idx.shape
     nb = 3 * E if bits is not None else E
-    dev = topk_idx.device
     d = x.shape[1] if x is not None else 0
     if out is None:
-        out = dict(counts=torch.empty(nb, dtype=torch.int32, device=dev),
-                   offsets=torch.empty(nb + 1, dtype=torch.int32, device=dev),
-                   perm=torch.empty(T * k, dtype=torch.int32, device=dev),
-                   inv_perm=torch.empty(T * k, dtype=torch.int32, device=dev),
-                   x_perm=torch.empty(T * k, d, dtype=torch.float16, device=dev) if x is not None else None)
+        out = dict(counts=_new(topk_idx, (nb,), torch.int32, stream),
+                   offsets=_new(topk_idx, (nb + 1,), torch.int32, stream),
+                   perm=_new(topk_idx, (T * k,), torch.int32, stream),
+                   inv_perm=_new(topk_idx, (T * k,), torch.int32, stream),
+                   x_perm=_new(topk_idx, (T * k, d), torch.float16, stream) if x is not None else None)
     if workspace is None:
         workspace = out.get("perm_ws")
     if workspace is None:
-        workspace = torch.empty(lib.moe_permute_workspace_bytes(T, E, k, int(bits is not None)),
-                                dtype=torch.uint8, device=dev)
+        workspace = _new(topk_idx, (lib.moe_permute_workspace_bytes(T, E, k, int(bits is not None)),), torch.uint8,
+                         stream, scratch=True)
     _check("moe_permute", lib.moe_permute(
         _ptr(topk_idx, torch.int32, "topk_idx"), _ptr(bits, torch.uint8, "bits"),
         _ptr(x, torch.bfloat16, "x"), T, d, E, k, _ptr(out["counts"], torch.int32),
@@ -243,7 +270,6 @@ def moe_route_permute(x, w_router, bias, k, forced_idx=None, bits=None, w_bit=No
     lib = load()
     T, d = x.shape
     E = w_router.shape[0]
-    dev = x.device
     nested = bits is not None or w_bit is not None
     nb = 3 * E if nested else E
     if out is None:
@@ -253,17 +279,17 @@ def moe_route_permute(x, w_router, bias, k, forced_idx=None, bits=None, w_bit=No
                            ("counts", (nb,), torch.int32), ("offsets", (nb + 1,), torch.int32),
                            ("perm", (T * k,), torch.int32), ("inv_perm", (T * k,), torch.int32)):
         if out.get(key) is None:
-            out[key] = torch.empty(*shape, dtype=dt, device=dev)
+            out[key] = _new(x, shape, dt, stream)
     if gather and out.get("x_perm") is None:
-        out["x_perm"] = torch.empty(T * k, d, dtype=torch.float16, device=dev)
+        out["x_perm"] = _new(x, (T * k, d), torch.float16, stream)
     bits_out = None
     if w_bit is not None:
         bits_out = out.get("bits")
         if bits_out is None:
-            bits_out = torch.empty(T, k, dtype=torch.uint8, device=dev)
+            bits_out = _new(x, (T, k), torch.uint8, stream)
     if workspace is None:
-        workspace = torch.empty(lib.moe_route_permute_workspace_bytes(T, d, E, k, int(nested)), dtype=torch.uint8,
-                                device=dev)
+        workspace = _new(x, (lib.moe_route_permute_workspace_bytes(T, d, E, k, int(nested)),), torch.uint8, stream,
+                         scratch=True)
     _check("moe_route_permute", lib.moe_route_permute(
         _ptr(x, torch.bfloat16, "x"), _ptr(w_router, torch.float32, "w_router"), _ptr(bias, torch.float32, "bias"),
         _ptr(forced_idx, torch.int32, "forced_idx"), _ptr(bits, torch.uint8, "bits"),
@@ -282,7 +308,7 @@ def moe_static_bits(topk_idx, width_of, E, bits=None, status=None, stream=None):
     lib = load()
     T, k = topk_idx.shape
     if bits is None:
-        bits = torch.empty(T, k, dtype=torch.uint8, device=topk_idx.device)
+        bits = _new(topk_idx, (T, k), torch.uint8, stream)
     _check("moe_static_bits", lib.moe_static_bits(
         _ptr(topk_idx, torch.int32, "topk_idx"), _ptr(width_of, torch.uint8, "width_of"), T, k, E,
         _ptr(bits, torch.uint8, "bits"), _ptr(status, torch.int32, "status"), _stream(stream)))
@@ -297,7 +323,7 @@ def moe_bit_gate(x, w_bit, bias_bit, topk_idx, bits=None, status=None, stream=No
     E = w_bit.shape[0]
     k = topk_idx.shape[1]
     if bits is None:
-        bits = torch.empty(T, k, dtype=torch.uint8, device=x.device)
+        bits = _new(x, (T, k), torch.uint8, stream)
     _check("moe_bit_gate", lib.moe_bit_gate(
         _ptr(x, torch.bfloat16, "x"), _ptr(w_bit, torch.float32, "w_bit"),
         _ptr(bias_bit, torch.float32, "bias_bit"), _ptr(topk_idx, torch.int32, "topk_idx"), T, d, E, k,
@@ -313,14 +339,13 @@ def moe_grouped_ffn_combine(x_perm, offsets, blobs, T, k, E, d, F, group, layout
                             residual=None, y=None, y_perm=None, workspace=None, status=None, stream=None):
     """The grouped FFN and the weighted combine in one call; returns (y, y_perm)."""
     lib = load()
-    dev = x_perm.device
     if y is None:
-        y = torch.empty(T, d, dtype=torch.bfloat16, device=dev)
+        y = _new(x_perm, (T, d), torch.bfloat16, stream)
     if y_perm is None:
-        y_perm = torch.empty(T * k, d, dtype=torch.float16, device=dev)
+        y_perm = _new(x_perm, (T * k, d), torch.float16, stream)
     if workspace is None:
-        workspace = torch.empty(lib.moe_ffn_combine_workspace_bytes(T, k, E, d, F, layout), dtype=torch.uint8,
-                                device=dev)
+        workspace = _new(x_perm, (lib.moe_ffn_combine_workspace_bytes(T, k, E, d, F, layout),), torch.uint8, stream,
+                         scratch=True)
     _check("moe_grouped_ffn_combine", lib.moe_grouped_ffn_combine(
         _ptr(x_perm, torch.float16, "x_perm"), _ptr(offsets, torch.int32, "offsets"), _ptr(blobs), T, k, E, d, F,
         group, layout, _ptr(perm, torch.int32, "perm"), _ptr(inv_perm, torch.int32, "inv_perm"),
@@ -335,10 +360,10 @@ def moe_grouped_ffn_wq(x_perm, offsets, blobs, T, E, d, F, group, layout, slot_o
     lib = load()
     rows = x_perm.shape[0]
     if workspace is None:
-        workspace = torch.empty(lib.moe_ffn_workspace_bytes(rows, E, d, F, layout), dtype=torch.uint8,
-                                device=x_perm.device)
+        workspace = _new(x_perm, (lib.moe_ffn_workspace_bytes(rows, E, d, F, layout),), torch.uint8, stream,
+                         scratch=True)
     if y_perm is None:
-        y_perm = torch.empty(rows, d, dtype=torch.float16, device=x_perm.device)
+        y_perm = _new(x_perm, (rows, d), torch.float16, stream)
     _check("moe_grouped_ffn_wq", lib.moe_grouped_ffn_wq(
         _ptr(x_perm, torch.float16, "x_perm"), _ptr(offsets, torch.int32, "offsets"), _ptr(blobs),
         _ptr(slot_of, torch.int32, "slot_of"), rows, T, E, d, F, group, layout, _ptr(workspace),
@@ -352,7 +377,7 @@ def moe_unpermute_combine(y_perm, inv_perm, topk_w, residual=None, y=None, strea
     T, k = topk_w.shape
     d = y_perm.shape[1]
     if y is None:
-        y = torch.empty(T, d, dtype=torch.bfloat16, device=y_perm.device)
+        y = _new(y_perm, (T, d), torch.bfloat16, stream)
     _check("moe_unpermute_combine", lib.moe_unpermute_combine(
         _ptr(y_perm, torch.float16, "y_perm"), _ptr(inv_perm, torch.int32, "inv_perm"),
         _ptr(topk_w, torch.float32, "topk_w"), _ptr(residual, torch.bfloat16, "residual"), T, k, d,
@@ -410,15 +435,6 @@ def _on(fn, first, *others):
     return _SAME if dev == torch.cuda.current_device() else _Other(dev)
 
 
-def _new(like, shape, dtype, stream):
-    """A new tensor on the device of `like`, for a call on `stream` (its memory
-    is not given out again before that stream has passed its release)."""
-    t = like.new_empty(shape, dtype=dtype)
-    if stream is not None:
-        t.record_stream(stream)
-    return t
-
-
 def _sized(fn, name, t, shape):
     if t is not None and t.shape != shape:
         raise ValueError(f"{fn}: {name} must have shape {shape}, got {tuple(t.shape)}")
@@ -454,7 +470,7 @@ def moe_route_scored(x, w_router, k, scoring="softmax", bias=None, n_groups=1, t
         if topk_w is None:
             topk_w = _new(x, (T, k), torch.float32, stream)
         if workspace is None:
-            workspace = _new(x, (lib.moe_route_scored_workspace_bytes(T, d, E),), torch.uint8, stream)
+            workspace = _new(x, (lib.moe_route_scored_workspace_bytes(T, d, E),), torch.uint8, stream, scratch=True)
         _check(fn, lib.moe_route_scored(
             _ptr(x, torch.bfloat16, "x"), _ptr(w_router, torch.float32, "w_router"), _ptr(bias, torch.float32, "bias"),
             T, d, E, k, _SCORING[scoring], n_groups, topk_groups, group_top, 1 if renorm else 0, scale,
@@ -592,7 +608,7 @@ def moe_grouped_ffn_mx(codes, scales, offsets, blobs, F, workspace=None, y_perm=
     _sized(fn, "y_perm", y_perm, (rows, d))
     with _on(fn, codes, scales, offsets, blobs, workspace, y_perm, status):
         if workspace is None:
-            workspace = _new(codes, (lib.moe_ffn_mx_workspace_bytes(rows, F),), torch.uint8, stream)
+            workspace = _new(codes, (lib.moe_ffn_mx_workspace_bytes(rows, F),), torch.uint8, stream, scratch=True)
         if y_perm is None:
             y_perm = _new(codes, (rows, d), torch.float16, stream)
         _check(fn, lib.moe_grouped_ffn_mx(
@@ -791,9 +807,9 @@ def moe_route_topk_noalloc(x, w_router, bias, k, forced_idx=None, topk_idx=None,
     T, d = x.shape
     E = w_router.shape[0]
     if topk_idx is None:
-        topk_idx = torch.empty(T, k, dtype=torch.int32, device=x.device)
+        topk_idx = _new(x, (T, k), torch.int32, stream)
     if topk_w is None:
-        topk_w = torch.empty(T, k, dtype=torch.float32, device=x.device)
+        topk_w = _new(x, (T, k), torch.float32, stream)
     _check("moe_route_topk_noalloc", lib.moe_route_topk_noalloc(
         _ptr(x, torch.bfloat16, "x"), _ptr(w_router, torch.float32, "w_router"),
         _ptr(bias, torch.float32, "bias"), _ptr(forced_idx, torch.int32, "forced_idx"), T, d, E, k,
