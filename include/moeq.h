@@ -437,10 +437,12 @@ MOE_API moe_status_t moe_mx_pack_ffn(const void* w_gate, const void* w_up, const
  *   codes, scales  the rows (moe_mx_quantize); offsets int32 [E + 1] (device;
  *                  moe_permute); mats E matrices (moe_mx_pack)
  *   out            [rows][N] of `out_dtype` (MOE_F32, MOE_BF16 or MOE_F16)
- * Products are exact, sums fp32, the result rounded once; rows that belong to
- * no expert keep what they held.  An fp16 output beyond the range flags
- * MOE_DEV_RANGE, offsets outside [0, rows] are clamped and flag
- * MOE_DEV_BAD_INDEX.  Requires N, K multiples of 128, E <= 256,
+ * Products are exact, sums fp32, the result rounded once.  An fp16 output
+ * beyond the range flags MOE_DEV_RANGE.  offsets rise from 0 to rows: a table
+ * that starts elsewhere, ends elsewhere or falls flags MOE_DEV_BAD_INDEX, its
+ * entries are clamped into [0, rows], and rows that belong to no expert keep
+ * what they held (pass the rows in use as `rows`, not a buffer's capacity).
+ * Requires N, K multiples of 128, E <= 256,
  * (rows / 128 + 1) * E * ceil(N / 256) < 2^30 and 16-byte aligned codes,
  * scales, mats and out. */
 MOE_API moe_status_t moe_mx_grouped_gemm(const void* codes, const void* scales, const int32_t* offsets,

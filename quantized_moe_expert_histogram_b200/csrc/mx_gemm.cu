@@ -134,14 +134,14 @@ __device__ __forceinline__ Tile decode_tile(int t, int cut, const int* tile_star
 // Tiles of 128 rows per expert -> exclusive scan over the experts, by all
 // threads; ends with warp 0 having written tile_start (the caller
 // synchronises).  Offsets are clamped into [0, rows]: no table can send a tile
-// outside.
+// outside.  One that does not rise from 0 to rows is flagged.
 __device__ __forceinline__ void build_tiles(const int32_t* offsets, int E, int rows, int NB, int32_t* status,
                                             int* tile_start, int* off_s) {
   const int tid = threadIdx.x, lane = tid & 31;
   for (int b = tid; b <= E; b += blockDim.x) {
     const int v = offsets[b];
     const int c = min(max(v, 0), rows);
-    if (c != v || (b == E ? v != rows : offsets[b + 1] < v)) flag_status(status, MOE_DEV_BAD_INDEX);
+    if (c != v || (b == 0 && v != 0) || (b == E ? v != rows : offsets[b + 1] < v)) flag_status(status, MOE_DEV_BAD_INDEX);
     off_s[b] = c;
   }
   __syncwarp();
