@@ -97,6 +97,8 @@ struct Params {
   void* out;
   uint8_t* out_scales;
   int32_t* status;
+  uint64_t wait_ns;  // limit of a wait
+  int stall;         // test hook: CTA 0 does not say that its first tile's sums are complete
 };
 
 struct Tile {
@@ -323,7 +325,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_mx_gemm(const __grid_constant__
       const uint8_t* sc = P.b_scales + static_cast<size_t>(T.e) * P.mat_stride +
                           static_cast<size_t>(T.n0 >> 7) * (P.K / 128) * 512;
       for (int kb = 0; kb < KB; ++kb) {
-        ok = warp_wait(empty(s), ph ^ 1, abort_flag, P.status);
+        ok = warp_wait(empty(s), ph ^ 1, abort_flag, P.status, P.wait_ns);
         if (!ok) break;
         if (warp == 0) {
           const uint32_t sb = P.K - kb * kKS > 128 ? 1024 : 512;
@@ -346,14 +348,11 @@ __global__ void __launch_bounds__(kThreads, 1) k_mx_gemm(const __grid_constant__
         if (++s == kStages) { s = 0; ph ^= 1; }
       }
     }
-    if (!ok) {  // the copies in flight land before the CTA goes
-      const uint64_t t0 = global_ns();
-      for (int i = 0; i < kStages; ++i) {
-        const int p = i < s ? ph : ph ^ 1;
-        while (!mbar_try(full(i), p) && global_ns() - t0 < kWaitLimitNs) {}
-      }
-      __syncwarp();
-    }
+    // The copies issued here land before the CTA goes, also where another warp
+    // gives up after the last of them was issued (a slot never used is complete).
+    uint64_t t0 = 0;
+    for (int i = 0; i < kStages; ++i) mbar_drain(full(i), i < s ? ph : ph ^ 1, P.wait_ns, t0);
+    __syncwarp();
   } else if (warp == 3) {
     // ---- row scales: four rows a lane, two 128-K words a stage --------------
     constexpr int G = 4;  // stages loaded ahead of the ones being written
@@ -385,7 +384,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_mx_gemm(const __grid_constant__
 #pragma unroll
         for (int g = 0; g < G; ++g) {
           if (kb0 + g < KB && ok) {
-            ok = warp_wait(empty(s), ph ^ 1, abort_flag, P.status);
+            ok = warp_wait(empty(s), ph ^ 1, abort_flag, P.status, P.wait_ns);
             if (ok) {
               uint8_t* dst = smem + kOffSA + s * kSA + lane * 16;
               *reinterpret_cast<uint4*>(dst) = cur[g][0];
@@ -414,7 +413,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_mx_gemm(const __grid_constant__
       const Tile T = decode_tile(t, cut, tile_start, off_s, E, P.N);
       const uint32_t id0 = idesc_mxf4(T.nn, 0), id1 = idesc_mxf4(T.nn, 1);
       if (tile >= 1) {  // the columns shared with the tile before
-        ok = warp_wait(acc_free(tile - 1), ((tile - 1) >> 1) & 1, abort_flag, P.status);
+        ok = warp_wait(acc_free(tile - 1), ((tile - 1) >> 1) & 1, abort_flag, P.status, P.wait_ns);
         if (!ok) break;
       }
       tc_fence_after();
@@ -423,10 +422,10 @@ __global__ void __launch_bounds__(kThreads, 1) k_mx_gemm(const __grid_constant__
       // compiler moved every operand through ordinary registers (60 cycles an
       // instruction instead of 10).
       auto stage = [&](auto two, uint32_t later) {
-        if (!warp_wait(full(s), ph, abort_flag, P.status)) return false;
+        if (!warp_wait(full(s), ph, abort_flag, P.status, P.wait_ns)) return false;
         // the products of kSets stages ago, which read this set of scale columns
         if (n >= kSets &&
-            !warp_wait(empty((n - kSets) % kStages), ((n - kSets) / kStages) & 1, abort_flag, P.status))
+            !warp_wait(empty((n - kSets) % kStages), ((n - kSets) / kStages) & 1, abort_flag, P.status, P.wait_ns))
           return false;
         tc_fence_after();
         const uint32_t sfa = tmem + kSF0 + (n % kSets) * kSFCols, sfb = sfa + 8;
@@ -455,12 +454,12 @@ __global__ void __launch_bounds__(kThreads, 1) k_mx_gemm(const __grid_constant__
       for (int kb = 0; kb < P.K / kKS && ok; ++kb) ok = stage(std::true_type{}, kb != 0);
       if (ok && P.K % kKS) ok = stage(std::false_type{}, P.K > kKS);
       if (!ok) break;
-      tc_commit(acc_full(tile));
+      if (!(P.stall && blockIdx.x == 0 && tile == 0)) tc_commit(acc_full(tile));
     }
     // every product issued here completes before tensor memory is released
     tc_commit(drain_bar);
     const uint64_t t0 = global_ns();
-    while (!mbar_try(drain_bar, 0) && global_ns() - t0 < kWaitLimitNs) {}
+    while (!mbar_try(drain_bar, 0) && global_ns() - t0 < P.wait_ns) {}
     __syncwarp();
   } else if (warp >= 4) {
     // ---- epilogue: lane = row of the tile, quadrant = warp % 4; the quadrant's
@@ -471,7 +470,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_mx_gemm(const __grid_constant__
     bool ok = true;
     for (int t = blockIdx.x; t < tiles && ok; t += gridDim.x, ++tile) {
       const Tile T = decode_tile(t, cut, tile_start, off_s, E, P.N);
-      ok = warp_wait(acc_full(tile), (tile >> 1) & 1, abort_flag, P.status);
+      ok = warp_wait(acc_full(tile), (tile >> 1) & 1, abort_flag, P.status, P.wait_ns);
       if (!ok) break;
       tc_fence_after();
       const uint32_t tb = tmem + (static_cast<uint32_t>(32 * q) << 16) + (tile & 1) * kAcc1;
@@ -508,7 +507,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_mx_gemm(const __grid_constant__
   if (lane == 0) mbar_arrive(exit_bar);
   if (warp == 3) {  // frees tensor memory once every warp has left its loop
     const uint64_t t0 = global_ns();
-    while (!mbar_try(exit_bar, 0) && global_ns() - t0 < 2 * kWaitLimitNs) {}
+    while (!mbar_try(exit_bar, 0) && global_ns() - t0 < 2 * P.wait_ns) {}
     __syncwarp();
     tc_fence_after();
     tmem_free(tmem, 512);
@@ -570,6 +569,8 @@ moe_status_t launch(const MxGemmArgs& a, cudaStream_t s) {
   P.out = a.out;
   P.out_scales = a.out_scales;
   P.status = a.status;
+  P.wait_ns = g_debug_stall ? kStallLimitNs : kWaitLimitNs;
+  P.stall = g_debug_stall;
   // shared-memory opt-in: a per-device attribute, set once per device (the
   // first call on a device precedes any stream capture)
   static std::atomic<uint64_t> attr_set{0};

@@ -73,6 +73,17 @@ __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, volatil
   return __all_sync(0xffffffffu, ok);
 }
 
+// Waits on the way out, whether or not the CTA is aborting: for a copy or a
+// product of this CTA to complete.  t0 (0 at first): when the first of a run
+// of waits did not succeed at once; the timer is read only then.
+__device__ __forceinline__ void mbar_drain(uint32_t bar, uint32_t parity, uint64_t limit_ns, uint64_t& t0) {
+  while (!mbar_try(bar, parity)) {
+    const uint64_t now = global_ns();
+    if (t0 == 0) t0 = now;
+    if (now - t0 > limit_ns) return;
+  }
+}
+
 // The copies and the tcgen05 instructions below are called by a whole
 // converged warp and elect the issuing lane inside (the same one every
 // time): their operands then stay in uniform registers.  Issued from a branch

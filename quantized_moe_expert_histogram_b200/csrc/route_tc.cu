@@ -62,6 +62,8 @@ struct Params {
   float* xsq;      // [S][T]
   int T, E, chunks, per_split;
   int32_t* status;
+  uint64_t wait_ns;  // limit of a wait
+  int stall;         // test hook: the first CTA does not say that its first sums are complete
 };
 
 __device__ __forceinline__ void mma_bf16(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
@@ -166,7 +168,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_route_tc(const __grid_constant_
     int armed = 0;
     for (int c = 0; c < n; ++c) {
       const int s = c % kStages;
-      ok = warp_wait(empty(s), ((c / kStages) & 1) ^ 1, abort_flag, P.status);
+      ok = warp_wait(empty(s), ((c / kStages) & 1) ^ 1, abort_flag, P.status, P.wait_ns);
       if (!ok) break;
       const uint32_t dst = smem_u32(smem + s * kStage);
       elect_expect_tx(full(s), kStage);
@@ -174,25 +176,25 @@ __global__ void __launch_bounds__(kThreads, 1) k_route_tc(const __grid_constant_
       for (int p = 0; p < 3; ++p) tma_load_3d(dst + kX + p * kW, &P.w, (c0 + c) * 64, e0, p, full(s));
       armed = c + 1;
     }
-    if (!ok) {  // the copies in flight land before the CTA goes
-      const uint64_t g0 = global_ns();
-      for (int c = max(0, armed - kStages); c < armed; ++c)
-        while (!mbar_try(full(c % kStages), (c / kStages) & 1) && global_ns() - g0 < kWaitLimitNs) {}
-      __syncwarp();
-    }
+    // the copies issued here land before the CTA goes, also where another warp
+    // gives up after the last of them was issued
+    uint64_t g0 = 0;
+    for (int c = max(0, armed - kStages); c < armed; ++c)
+      mbar_drain(full(c % kStages), (c / kStages) & 1, P.wait_ns, g0);
+    __syncwarp();
   } else if (warp == 1) {
     bool ok = true;
     const uint64_t d0 = desc_sw128(smem_u32(smem));
     for (int c = 0; c < n; ++c) {
       const int s = c % kStages;
-      ok = warp_wait(full(s), (c / kStages) & 1, abort_flag, P.status);
-      if (ok && c > 0) ok = warp_wait(hi_free, (c - 1) & 1, abort_flag, P.status);
+      ok = warp_wait(full(s), (c / kStages) & 1, abort_flag, P.status, P.wait_ns);
+      if (ok && c > 0) ok = warp_wait(hi_free, (c - 1) & 1, abort_flag, P.status, P.wait_ns);
       if (!ok) break;
       tc_fence_after();
       const uint64_t bx = d0 + s * (kStage >> 4), aw = bx + (kX >> 4);
 #pragma unroll
       for (int k = 0; k < 4; ++k) mma_bf16(tmem, aw + 2 * k, bx + 2 * k, kIdesc, k != 0);
-      tc_commit(hi_full);
+      if (!(P.stall && (blockIdx.x | blockIdx.y | blockIdx.z) == 0 && c == 0)) tc_commit(hi_full);
 #pragma unroll
       for (int p = 1; p < 3; ++p)
 #pragma unroll
@@ -203,7 +205,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_route_tc(const __grid_constant_
     if (ok) tc_commit(ml_full);
     tc_commit(drain_bar);  // every product completes before tensor memory is released
     const uint64_t g0 = global_ns();
-    while (!mbar_try(drain_bar, 0) && global_ns() - g0 < kWaitLimitNs) {}
+    while (!mbar_try(drain_bar, 0) && global_ns() - g0 < P.wait_ns) {}
     __syncwarp();
   } else if (warp >= 4) {
     // lane = expert 32 q + lane of the tile, 128 tokens; as a norm thread, token `row`
@@ -218,7 +220,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_route_tc(const __grid_constant_
     for (int c = 0; c < n; ++c) {
       const int s = c % kStages;
       if (norms) {
-        ok = warp_wait(full(s), (c / kStages) & 1, abort_flag, P.status);
+        ok = warp_wait(full(s), (c / kStages) & 1, abort_flag, P.status, P.wait_ns);
         if (!ok) break;
         const uint8_t* xr = smem + s * kStage + row * 128;
 #pragma unroll
@@ -234,7 +236,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_route_tc(const __grid_constant_
         __syncwarp();
         if (lane == 0) mbar_arrive(empty(s));
       }
-      ok = warp_wait(hi_full, c & 1, abort_flag, P.status);
+      ok = warp_wait(hi_full, c & 1, abort_flag, P.status, P.wait_ns);
       if (!ok) break;
       tc_fence_after();
 #pragma unroll
@@ -249,7 +251,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_route_tc(const __grid_constant_
       __syncwarp();
       if (lane == 0) mbar_arrive(hi_free);
     }
-    if (ok && n > 0) ok = warp_wait(ml_full, 0, abort_flag, P.status);
+    if (ok && n > 0) ok = warp_wait(ml_full, 0, abort_flag, P.status, P.wait_ns);
     if (ok) {
       tc_fence_after();
       const int e = e0 + 32 * q + lane;
@@ -276,7 +278,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_route_tc(const __grid_constant_
   if (lane == 0) mbar_arrive(exit_bar);
   if (warp == 2) {  // frees tensor memory once every warp has left its loop
     const uint64_t g0 = global_ns();
-    while (!mbar_try(exit_bar, 0) && global_ns() - g0 < 2 * kWaitLimitNs) {}
+    while (!mbar_try(exit_bar, 0) && global_ns() - g0 < 2 * P.wait_ns) {}
     __syncwarp();
     tc_fence_after();
     tmem_free(tmem, 512);
@@ -358,6 +360,8 @@ moe_status_t launch_route_partials_tc(const void* x, const float* w_router, int 
   P.chunks = p.chunks;
   P.per_split = p.per_split;
   P.status = status;
+  P.wait_ns = g_debug_stall ? kStallLimitNs : kWaitLimitNs;
+  P.stall = g_debug_stall;
   // shared-memory opt-in: a per-device attribute, set once per device (the
   // first call on a device precedes any stream capture)
   static std::atomic<uint64_t> attr_set{0};

@@ -790,7 +790,8 @@ def moe_debug_route_fused(mode):
 
 
 def moe_debug_ffn_timeout(enable):
-    """Test hook: a withheld arrive and a 20 ms wait limit in the tensor-core FFN."""
+    """Test hook: a withheld arrive and a 20 ms wait limit in the tensor-core
+    FFN, the MXFP4 product and the scored router's tensor-core logits."""
     load().moe_debug_ffn_timeout(int(bool(enable)))
 
 
