@@ -142,6 +142,34 @@ def ffn(x, wg, wu, wd):
     return q @ wd.T, y + (hi - lo) @ np.abs(wd).T
 
 
+def exact_rows(rng, rows, K, log2_scale=0):
+    """Values [rows][K] on the grid times 2^log2_scale, a 6 in every block:
+    they are their own MXFP4 form, all scales equal, so that products of two
+    such operands are multiples of a quarter of their scales and fp32 sums of
+    up to 2^24 / (36 * 4) of them are exact in any order."""
+    v = GRID[rng.integers(0, 8, (rows, K // BLOCK, BLOCK))] * rng.choice([-1.0, 1.0], (rows, K // BLOCK, BLOCK))
+    at = rng.integers(0, BLOCK, (rows, K // BLOCK, 1))
+    np.put_along_axis(v, at, 6.0 * rng.choice([-1.0, 1.0], at.shape), axis=2)
+    return v.reshape(rows, K) * 2.0 ** log2_scale
+
+
+def hidden(x, wg, wu):
+    """(q, lo, hi): hq = MXFP4 of silu(x wg) (x wu) for operands whose fp32
+    sums are exact, and the least and largest value of each element that the
+    fp32 SwiGLU's rounding (as in ffn) can make of it; lo = hi where no
+    rounding point is that near."""
+    g, u = x @ wg.T, x @ wu.T
+    h = g / (1 + np.exp(-g)) * u
+    eps = np.abs(h) * (6 + 1.2 * np.abs(g)) * 2.0 ** -23
+    q = rounded(h)
+    lo, hi = q.copy(), q.copy()
+    for byte in (scale_bytes(np.maximum(np.abs(h) - eps, 0)), scale_bytes(np.abs(h) + eps)):
+        for v in (h - eps, h + eps):
+            c = values(encode(v, byte), byte)
+            lo, hi = np.minimum(lo, c), np.maximum(hi, c)
+    return q, lo, hi
+
+
 def half_step(y, dtype_eps, tiny):
     """Half a step of a floating type: eps/2 relative, half the smallest subnormal near zero."""
     return np.abs(y) * dtype_eps / 2 + tiny / 2
