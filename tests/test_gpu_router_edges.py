@@ -102,3 +102,59 @@ def test_weights_of_scores_that_vanish(top, renorm, T):
         np.testing.assert_array_equal(idx.cpu().numpy(), ref)
         # (not renormalised, a score below fp32's range is 0 or subnormal: 2^-149 apart)
         np.testing.assert_allclose(wt.cpu().numpy(), rw, rtol=1e-5, atol=0 if renorm else 2.0 ** -148)
+
+
+def check_picks(x, w, k, bias=None, rtol=1e-5, **kw):
+    idx, wt = moeq.moe_route_scored(x.cuda(), w.cuda(), k, bias=None if bias is None else bias.cuda(), **kw)
+    ref, rw, _ = M.route_scored(x.double().numpy(), w.double().numpy(), k,
+                                bias=None if bias is None else bias.double().numpy(), **kw)
+    np.testing.assert_array_equal(idx.cpu().numpy(), ref)
+    np.testing.assert_allclose(wt.cpu().numpy(), rw, rtol=rtol, atol=1e-30)   # (RTOL of the scored router's tests)
+
+
+@pytest.mark.parametrize("T", [1, 4, 33, 150])
+@pytest.mark.parametrize("scoring", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("E,G,kept,top,k", [(256, 32, 7, 2, 8), (256, 32, 31, 1, 16), (256, 16, 3, 2, 16), (64, 32, 4, 2, 8),
+                                            (32, 32, 9, 1, 9), (160, 32, 2, 1, 8), (96, 16, 16, 2, 5), (180, 20, 5, 2, 6),
+                                            (99, 11, 4, 2, 7)])
+def test_many_groups(E, G, kept, top, k, scoring, T):
+    """Two lanes, and one, to a group; group counts that divide no warp."""
+    g = torch.Generator().manual_seed(60 + G)
+    x, w = torch.randn(T, 256, generator=g).bfloat16(), torch.randn(E, 256, generator=g) * 0.06
+    b = torch.randn(E, generator=g) * 0.05
+    kw = dict(scoring=scoring, n_groups=G, topk_groups=kept, group_top=top)
+    check_picks(x, w, k, bias=b, **kw)
+    check_picks(x, w, k, renorm=False, **kw)
+    w = w[torch.arange(E) % 7]                   # ties inside groups and between them
+    check_picks(x, w, k, **kw)
+    check_picks(x, w, k, bias=torch.zeros(E), **kw)
+
+
+@pytest.mark.parametrize("T", [2, 40])
+@pytest.mark.parametrize("scoring", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("E,k", [(256, 16), (256, 1), (48, 16), (16, 16)])
+def test_all_experts_equal(E, k, scoring, T):
+    """More experts tied at the cut than a warp has lanes."""
+    x = torch.randn(T, 96, generator=torch.Generator().manual_seed(61)).bfloat16()
+    w = torch.zeros(E, 96)
+    for bias in (None, torch.zeros(E), torch.full((E,), 1e30), torch.full((E,), -1e30)):
+        check_picks(x, w, k, bias=bias, scoring=scoring)
+        check_picks(x, w, k, bias=bias, scoring=scoring, n_groups=4 if E >= 48 else 1, topk_groups=2 if E >= 48 else 1,
+                    group_top=2)
+
+
+@pytest.mark.parametrize("T", [3, 40])
+@pytest.mark.parametrize("scoring", ["softmax", "sigmoid"])
+def test_biases_out_of_range(scoring, T):
+    g = torch.Generator().manual_seed(62)
+    x, w = torch.randn(T, 128, generator=g).bfloat16(), torch.randn(40, 128, generator=g) * 0.1
+    b = torch.randn(40, generator=g) * 0.05
+    inf = float("inf")
+    for places, value in (([3, 30], inf), ([3, 4, 30], 3e38), ([5, 6], float("nan")), ([0, 39], -3e38), (list(range(35)), -inf)):
+        c = b.clone()
+        c[places] = value
+        for kw in (dict(), dict(n_groups=8, topk_groups=3, group_top=2), dict(n_groups=8, topk_groups=3)):
+            check_picks(x, w, 6, bias=c, scoring=scoring, **kw)
+    c = b.clone()
+    c[3], c[4], c[20] = inf, -inf, float("nan")  # a group's sum is NaN, and counts as -inf
+    check_picks(x, w, 6, bias=c, scoring=scoring, n_groups=8, topk_groups=3, group_top=2)
