@@ -141,6 +141,8 @@ class MxMoELayer:
         T = x.shape[0]
         if T > self.max_tokens:
             raise ValueError(f"T={T} exceeds max_tokens={self.max_tokens}")
+        if residual is not None and residual.shape != x.shape:
+            raise ValueError(f"MxMoELayer.forward: residual must have shape {tuple(x.shape)}, got {tuple(residual.shape)}")
         with moeq._on("MxMoELayer.forward", self.buf["y"], x, residual):
             v = self.views(T)
             moeq.moe_route_scored(x, self.w_router, self.k, bias=self.bias, topk_idx=v["topk_idx"], topk_w=v["topk_w"],

@@ -182,6 +182,12 @@ def _new(like, shape, dtype, stream, scratch=False):
     return t
 
 
+def _holds(fn, name, t, n):
+    """t, if given, has the n elements that the call reads or writes."""
+    if t is not None and t.numel() < n:
+        raise ValueError(f"{fn}: {name} must hold {n} elements, got {tuple(t.shape)}")
+
+
 def moe_blob_bytes(d, F, group, layout):
     return int(load().moe_blob_bytes(d, F, group, layout))
 
@@ -339,6 +345,8 @@ def moe_grouped_ffn_combine(x_perm, offsets, blobs, T, k, E, d, F, group, layout
                             residual=None, y=None, y_perm=None, workspace=None, status=None, stream=None):
     """The grouped FFN and the weighted combine in one call; returns (y, y_perm)."""
     lib = load()
+    _holds("moe_grouped_ffn_combine", "residual", residual, T * d)
+    _holds("moe_grouped_ffn_combine", "y", y, T * d)
     if y is None:
         y = _new(x_perm, (T, d), torch.bfloat16, stream)
     if y_perm is None:
@@ -376,6 +384,9 @@ def moe_unpermute_combine(y_perm, inv_perm, topk_w, residual=None, y=None, strea
     lib = load()
     T, k = topk_w.shape
     d = y_perm.shape[1]
+    for name, t, n in (("y_perm", y_perm, T * k * d), ("inv_perm", inv_perm, T * k), ("residual", residual, T * d),
+                       ("y", y, T * d)):
+        _holds("moe_unpermute_combine", name, t, n)
     if y is None:
         y = _new(y_perm, (T, d), torch.bfloat16, stream)
     _check("moe_unpermute_combine", lib.moe_unpermute_combine(
