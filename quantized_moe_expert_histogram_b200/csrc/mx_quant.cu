@@ -267,7 +267,7 @@ moe_status_t moe_mx_quantize(const void* x, int dtype, int rows, int K, size_t l
               dtype);
     return MOE_ERR_INVALID_ARG;
   }
-  if (!inv_perm && k != 1) {
+  if (!inv_perm && k != 1 && rows > 0) {
     set_error("%s: k=%d places a row need inv_perm", fn, k);
     return MOE_ERR_INVALID_ARG;
   }

@@ -6,6 +6,7 @@ import torch
 
 from oracle import mx_oracle as M
 from quantized_moe_expert_histogram_b200 import build, moeq
+from quantized_moe_expert_histogram_b200.layer import MxMoELayer
 
 pytestmark = pytest.mark.gpu
 
@@ -81,3 +82,22 @@ def test_ffn_stages(rows_of, d, F):
         # far below |y|: F 2^-23 times a sum of F magnitudes, beside a sum that is about its root
         assert np.median(lim) < (1.5 * F ** 1.5 * 2.0 ** -23 + 2.0 ** -9) * np.median(np.abs(ref))
     assert near < 1e-3 * hq.size
+
+
+def test_empty_batches():
+    """No tokens, no rows: outputs of no rows, from each call and the layer."""
+    d, E, k, F = 256, 8, 2, 128
+    blobs = moeq.moe_mx_pack_ffn(normal(E, F, d, seed=6), normal(E, F, d, seed=7), normal(E, d, F, seed=8))
+    w = normal(E, d, seed=9)
+    x = normal(4, d, seed=10, dtype=torch.bfloat16)
+    idx, wt = moeq.moe_route_scored(x[:0], w, k)
+    assert idx.shape == wt.shape == (0, k)
+    codes, scales = moeq.moe_mx_quantize(x[:0], inv_perm=torch.empty(0, k, dtype=torch.int32, device="cuda"), k=k)
+    assert codes.shape == (0, d // 2) and moeq.moe_mx_dequantize(codes, scales).shape == (0, d)
+    off = torch.zeros(E + 1, dtype=torch.int32, device="cuda")
+    assert moeq.moe_grouped_ffn_mx(codes, scales, off, blobs, F).shape == (0, d)
+    assert moeq.moe_mx_grouped_gemm(codes, scales, off, moeq.moe_mx_pack(normal(E, 128, d, seed=11)), 128).shape == (0, 128)
+    layer = MxMoELayer(d, E, k, F, w, blobs, 4)
+    want = layer.forward(x).clone()
+    assert layer.forward(x[:0]).shape == (0, d) and layer.buf["status"].item() == 0
+    assert torch.equal(layer.forward(x), want)

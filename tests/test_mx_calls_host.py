@@ -71,3 +71,12 @@ def test_layer_refuses_a_residual_of_another_shape(lib):
         with pytest.raises(ValueError, match="residual"):
             layer.forward(bf16(4, 128), residual=bf16(*shape))
     assert not lib.calls
+
+
+def test_quantising_no_rows_needs_no_places():
+    """An empty permutation has no address."""
+    from quantized_moe_expert_histogram_b200 import build
+    build.build()
+    L = moeq.open_library()
+    assert L.moe_mx_quantize(None, 1, 0, 64, 64, None, 4, None, None, None, None) == 0
+    assert L.moe_mx_quantize(4096, 1, 4, 64, 64, None, 4, 4096, 4096, None, None) == 1
