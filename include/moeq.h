@@ -610,16 +610,20 @@ MOE_API void moe_debug_set_trace(void* host_mapped_ints);
 MOE_API void moe_debug_route_fused(int mode);
 
 /* Test hook of the on-device failure path: while enabled, the tensor-core
- * FFN kernels, the MXFP4 product and the scored router's tensor-core logits
- * give every bounded wait a 20 ms limit (instead of 2 s), and CTA 0 withholds
- * one arrive that has no copy behind it: in the FFN's gate/up kernel the
- * release of its first tile's accumulators (the MMA warp's wait for its next
- * tile runs out whenever it has one), in the MXFP4 product and the router the
- * word that its first tile's (chunk's) sums are complete.  The CTA then sets
- * MOE_DEV_TIMEOUT in `status`, drains its copies and MMAs, frees its tensor
- * memory and returns; that call's outputs are undefined.  0 (the default)
- * disables it.  Process-wide. */
+ * FFN kernels give every bounded wait a 20 ms limit (instead of 2 s), and in
+ * the gate/up kernel the epilogue of CTA 0 withholds the release of its
+ * first tile's accumulators -- an arrive with no copy behind it -- so that
+ * the MMA warp's wait for its next tile runs out whenever CTA 0 has more than
+ * one tile.  The CTA then sets MOE_DEV_TIMEOUT in `status`, drains its
+ * copies and MMAs, frees its tensor memory and returns; that call's outputs
+ * are undefined.  0 (the default) disables it.  Process-wide. */
 MOE_API void moe_debug_ffn_timeout(int enable);
+
+/* The same for the MXFP4 product (and so the MXFP4 FFN) and the scored
+ * router's tensor-core logits: waits of 20 ms at most, and CTA 0 withholds
+ * the word that its first tile's (router: chunk's) sums are complete, so that
+ * its epilogue's wait runs out. */
+MOE_API void moe_debug_mx_timeout(int enable);
 
 #ifdef __cplusplus
 }

@@ -472,10 +472,6 @@ struct RoutePartials {
 moe_status_t launch_route_partials_tc(const void* x, const float* w_router, int T, int d, int E, void* workspace,
                                       int32_t* status, RoutePartials* out, cudaStream_t s);
 size_t route_tc_workspace_bytes(int T, int d, int E);
-// test hook (moe_debug_ffn_timeout): an arrive withheld and waits of 20 ms at
-// most in the kernels that wait on barriers of their own
-extern int g_debug_stall;
-constexpr uint64_t kStallLimitNs = 20000000ull;
 extern int g_route_fused;  // test hook: 1 default, 0 no fp64 cluster paths
 constexpr int kTinyGateAssign = 32;   // assignments of the cluster bit gate (T*k)
 static_assert(kTinyGateAssign <= 32, "TinyGateSmem holds 32 assignments");

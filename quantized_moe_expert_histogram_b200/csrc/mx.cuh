@@ -97,5 +97,6 @@ struct MxGemmArgs {
 enum { kMxOutF16 = 0, kMxOutBf16 = 1, kMxOutF32 = 2, kMxOutSwiglu = 3 };
 moe_status_t launch_mx_gemm(const MxGemmArgs& a, cudaStream_t s);
 constexpr int kMxMaxExperts = 256;
+extern int g_mx_stall;  // test hook moe_debug_mx_timeout
 
 }  // namespace moeq

@@ -569,8 +569,8 @@ moe_status_t launch(const MxGemmArgs& a, cudaStream_t s) {
   P.out = a.out;
   P.out_scales = a.out_scales;
   P.status = a.status;
-  P.wait_ns = g_debug_stall ? kStallLimitNs : kWaitLimitNs;
-  P.stall = g_debug_stall;
+  P.wait_ns = g_mx_stall ? kStallLimitNs : kWaitLimitNs;
+  P.stall = g_mx_stall;
   // shared-memory opt-in: a per-device attribute, set once per device (the
   // first call on a device precedes any stream capture)
   static std::atomic<uint64_t> attr_set{0};
@@ -598,6 +598,8 @@ moe_status_t launch(const MxGemmArgs& a, cudaStream_t s) {
 }
 
 }  // namespace
+
+int g_mx_stall = 0;
 
 moe_status_t launch_mx_gemm(const MxGemmArgs& a, cudaStream_t s) {
   if (a.rows == 0) return MOE_OK;
@@ -728,5 +730,7 @@ moe_status_t moe_grouped_ffn_mx(const void* codes, const void* scales, const int
   a.out_scales = nullptr;
   return launch_mx_gemm(a, static_cast<cudaStream_t>(stream));
 }
+
+void moe_debug_mx_timeout(int enable) { g_mx_stall = enable ? 1 : 0; }
 
 }  // extern "C"

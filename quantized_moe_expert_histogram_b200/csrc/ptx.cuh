@@ -42,6 +42,7 @@ __device__ __forceinline__ uint64_t global_ns() {
 }
 
 constexpr uint64_t kWaitLimitNs = 2000000000ull;  // 2 s: only reached when something is broken
+constexpr uint64_t kStallLimitNs = 20000000ull;   // under the test hook moe_debug_mx_timeout
 
 // Bounded wait: false when the CTA is aborting (its flag is set by whichever
 // role first ran out of time).

@@ -39,6 +39,7 @@
 #include <atomic>
 #include <mutex>
 
+#include "mx.cuh"
 #include "ptx.cuh"
 
 namespace moeq {
@@ -360,8 +361,8 @@ moe_status_t launch_route_partials_tc(const void* x, const float* w_router, int 
   P.chunks = p.chunks;
   P.per_split = p.per_split;
   P.status = status;
-  P.wait_ns = g_debug_stall ? kStallLimitNs : kWaitLimitNs;
-  P.stall = g_debug_stall;
+  P.wait_ns = g_mx_stall ? kStallLimitNs : kWaitLimitNs;
+  P.stall = g_mx_stall;
   // shared-memory opt-in: a per-device attribute, set once per device (the
   // first call on a device precedes any stream capture)
   static std::atomic<uint64_t> attr_set{0};

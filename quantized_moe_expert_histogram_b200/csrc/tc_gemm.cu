@@ -901,6 +901,7 @@ bool encode(CUtensorMap* m, CUtensorMapDataType dt, int rank, const void* base, 
 }
 
 int* g_trace = nullptr;  // test hook: host-mapped progress record
+int g_debug_stall = 0;   // test hook: a withheld arrive and a 20 ms wait limit
 
 // SM count of the current device (cached per device).
 int sm_count() {
@@ -971,7 +972,7 @@ moe_status_t make_params(TcParams& P, const FfnArgs& a, const __half* act, int r
   P.group = a.group;
   P.status = a.status;
   P.trace = g_trace;
-  P.wait_ns = g_debug_stall ? kStallLimitNs : kWaitLimitNs;
+  P.wait_ns = g_debug_stall ? 20000000ull : kWaitLimitNs;
   P.debug_stall = g_debug_stall;
   return MOE_OK;
 }
@@ -995,8 +996,6 @@ moe_status_t launch_one(const TcParams& P, bool pdl, cudaStream_t s) {
 }
 
 }  // namespace
-
-int g_debug_stall = 0;
 
 bool tc_supported(const FfnArgs& a) {
   return get_encode() != nullptr && a.d % 128 == 0 && a.F % 128 == 0 &&

@@ -88,6 +88,7 @@ _SIGS = {
     "moe_debug_force_regime": (None, [_c_i]),
     "moe_debug_set_trace": (None, [_c_p]),
     "moe_debug_ffn_timeout": (None, [_c_i]),
+    "moe_debug_mx_timeout": (None, [_c_i]),
     "moe_debug_route_fused": (None, [_c_i]),
 }
 
@@ -801,9 +802,13 @@ def moe_debug_route_fused(mode):
 
 
 def moe_debug_ffn_timeout(enable):
-    """Test hook: a withheld arrive and a 20 ms wait limit in the tensor-core
-    FFN, the MXFP4 product and the scored router's tensor-core logits."""
+    """Test hook: a withheld arrive and a 20 ms wait limit in the tensor-core FFN."""
     load().moe_debug_ffn_timeout(int(bool(enable)))
+
+
+def moe_debug_mx_timeout(enable):
+    """Test hook: the same in the MXFP4 product and the scored router's tensor-core logits."""
+    load().moe_debug_mx_timeout(int(bool(enable)))
 
 
 def moe_debug_set_trace(pinned_int32=None):

@@ -16,7 +16,7 @@ def _hooks():
     build.build()
     moeq.load()
     yield
-    moeq.moe_debug_ffn_timeout(0)
+    moeq.moe_debug_mx_timeout(0)
 
 
 def normal(*shape, seed, std=1.0):
@@ -24,7 +24,7 @@ def normal(*shape, seed, std=1.0):
 
 
 def product():
-    # 40 x 8 tiles of 128 rows x 256 outputs: CTA 0 has a second one, whose columns it waits for
+    # 40 x 8 tiles of 128 rows x 256 outputs: CTA 0 has a second one
     codes, scales = moeq.moe_mx_quantize(normal(5120, 512, seed=1))
     mats = moeq.moe_mx_pack(normal(1, 2048, 512, seed=2, std=0.05))
     off = torch.tensor([0, 5120], dtype=torch.int32, device="cuda")
@@ -51,10 +51,10 @@ def test_bounded_waits_run_out_and_the_next_call_is_exact(case):
     st = torch.zeros(1, dtype=torch.int32, device="cuda")
     want = call(st)
     assert st.item() == 0
-    moeq.moe_debug_ffn_timeout(1)
+    moeq.moe_debug_mx_timeout(1)
     call(st)                         # returns instead of hanging
     assert st.item() & moeq.DEV_TIMEOUT
-    moeq.moe_debug_ffn_timeout(0)
+    moeq.moe_debug_mx_timeout(0)
     st.zero_()
     got = call(st)
     assert st.item() == 0
