@@ -35,13 +35,18 @@
 // 64 experts, 1 token 23.8 -> 20.1 us, product of 512 x 4096 x 4096 14.1 ->
 // 13.1 us.
 //
-// What bounds it where experts have many rows: the way from L2 to the SMs.  A
-// stage is 52 KB for 512 cycles of products; 32768 rows of 64 experts, 2048 x
-// 2048 and 2048 x 1024 (an FFN: 160 us, 2.6 PFLOP/s) load and store 1.6 GB
-// through it, 16384 rows of 8 experts at d = 4096, F = 14336 (1.46 ms, 4.0
-// PFLOP/s) 17.5 GB: 10 and 12 TB/s.  Sixteen epilogue warps in place of eight
-// took 182 us for the first; pairs of SMs that share a weight tile (half its
-// bytes) were 5 % faster at 2048 rows an expert and up to 18 % slower below.
+// Where experts have many rows the bound is not established.  A stage is 52 KB
+// for 512 cycles of products; 32768 rows of 64 experts, 2048 x 2048 and 2048 x
+// 1024 (an FFN: 160 us in a short run, 2.6 PFLOP/s; 182 in a long one) load
+// and store 1.6 GB between L2 and the SMs, 16384 rows of 8 experts at d =
+// 4096, F = 14336 (1.46 ms in a short run, 4.0 PFLOP/s; 1.60 in a long one,
+// under the power cap) 17.5 GB: 10 and 12 TB/s, with the tensor pipe 32 to
+// 43 % busy.  Pairs of SMs that share a weight tile (two thirds of a stage's
+// bytes) were 5 % faster at 2048 rows an expert and up to 18 % slower below,
+// so bytes are not all of it; a stage's six scale copies and four products
+// wait for the products of two stages before (two sets of scale columns),
+// which was not timed apart.  Sixteen epilogue warps in place of eight took 182
+// us for the first.
 //
 // Every wait is bounded; on a timeout the CTA raises MOE_DEV_TIMEOUT, lets its
 // copies land, frees tensor memory and returns.
@@ -189,7 +194,8 @@ __device__ __forceinline__ bool store_group(void* out_v, uint8_t* out_scales, ui
 #pragma unroll
     for (int j = 0; j < 32; ++j) {
       // (a fast division, 2 ulp: the exact one's path for tiny operands, which the rows
-      // past the tile's hold, took 4 times as long as all the rest of the kernel)
+      // past the tile's hold, took 4 times as long as all the rest of the kernel.  For g
+      // below -87.3, where |silu(g)| < 2^-119, it gives 0.)
       const float gv = __uint_as_float(g[j]);
       h[j] = __fdividef(gv, 1.0f + __expf(-gv)) * __uint_as_float(u[j]);
       m = max(m, __float_as_uint(h[j]) & 0x7FFFFFFFu);

@@ -15,8 +15,10 @@
 // A block's work is one pass (a persistent grid of 8 blocks an SM took 6 to 8 %
 // longer), and what is used once goes through the caches as streaming: fp32
 // rows in (134.0 -> 125.5 us for 28673 x 4096 to MXFP4 and back), bf16 values
-// out (41.5 -> 35.2 us for 4096 x 2048 to 8 places and back).  That is 93 % and
-// 81 % of the copy bandwidth.
+// out (41.5 -> 35.2 us for 4096 x 2048 to 8 places and back).  In a captured
+// graph the two take 122 and 31.6 us: 96 % and 90 % of the copy bandwidth.
+// Packing weights (offline): 64 experts of 3 x 2048 x 1024 in 227 us from bf16
+// (4.5 TB/s) and 286 us from fp32 (6.4 TB/s); scale bytes leave one by one.
 #include "mx.cuh"
 
 namespace moeq {

@@ -31,7 +31,7 @@
 // the tokens each) while the eight of mid and lo run into the second
 // accumulator; both take all 512 columns.  80 KB a stage for 12 x 128 cycles
 // of instructions: 53 bytes a cycle and SM, about what L2 delivers.  8191
-// tokens, 256 experts, d = 4096: 51 us (1.0 PFLOP/s of bf16 products, 63 % of
+// tokens, 256 experts, d = 4096: 51 us (1.0 PFLOP/s of bf16 products, 61 % of
 // the measured rate, on 128 of the 148 SMs; the tensor pipe is busy 61 % of the
 // time; fp32 sums took 683 us with their selection).
 #include <cudaTypedefs.h>

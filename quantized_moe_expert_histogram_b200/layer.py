@@ -96,7 +96,9 @@ class MxMoELayer:
     moe_mx_quantize (each token's row once, to its experts' places) ->
     moe_grouped_ffn_mx -> moe_unpermute_combine.  It owns the device buffers;
     ``forward`` allocates nothing and can be captured into a graph (after one
-    call on the device)."""
+    call on the device).  Calls of one layer, and graphs that hold them, share
+    its buffers: run them in order.  ``buf["status"]`` gathers the calls'
+    status bits until it is cleared."""
 
     def __init__(self, d, E, k, F, w_router, blobs, max_tokens, bias=None, scoring="softmax", n_groups=1,
                  topk_groups=1, group_top=1, renorm=True, scale=1.0, device="cuda"):
