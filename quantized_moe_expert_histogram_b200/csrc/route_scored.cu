@@ -581,8 +581,7 @@ __device__ __forceinline__ void select_block(const Scored& A, Row<P>* rows, int 
     wt = weight64(A, s64, lane);
   } else {
     const float l = row.l[mine];
-    // (sigmoid(l) = e^l (1 + tiny) below -60, and e^-l soon overflows)
-    float s = A.sigmoid ? (l < -60.f ? expf(l) : 1.0f / (1.0f + expf(-l))) : expf(l - row_max), top = 0.f;
+    float top = 0.f;
     if (A.renorm) {
       top = lane < k ? l : -INFINITY;
 #pragma unroll
@@ -593,9 +592,16 @@ __device__ __forceinline__ void select_block(const Scored& A, Row<P>* rows, int 
       wt = weight64(A, A.sigmoid ? 1.0 / (1.0 + exp(-static_cast<double>(l)))
                                  : exp(static_cast<double>(l) - row_max) / row_sum, lane);
     } else {
+      float s;
+      if (!A.sigmoid) {
+        s = expf(l - (A.renorm ? top : row_max));
+      } else if (A.renorm && top < -8.f) {
+        // all scores times e^-top: those that would leave fp32's range keep their ratio to the largest
+        s = expf(l - top) / (1.0f + expf(l));
+      } else {  // (sigmoid(l) = e^l (1 + tiny) below -60, and e^-l soon overflows)
+        s = l < -60.f ? expf(l) : 1.0f / (1.0f + expf(-l));
+      }
       if (A.renorm) {
-        // scores so small that they leave fp32's range: taken from the largest
-        if (!A.sigmoid || top < -60.f) s = expf(l - top);
         float sum = lane < k ? s : 0.f;
 #pragma unroll
         for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);

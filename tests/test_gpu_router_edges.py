@@ -104,6 +104,26 @@ def test_weights_of_scores_that_vanish(top, renorm, T):
         np.testing.assert_allclose(wt.cpu().numpy(), rw, rtol=1e-5, atol=0 if renorm else 2.0 ** -148)
 
 
+@pytest.mark.parametrize("T", [3, 40])
+@pytest.mark.parametrize("top", [30.0, 0.0, -7.5, -8.5, -20.0, -59.0, -61.0, -100.0, -400.0])
+@pytest.mark.parametrize("scoring", ["softmax", "sigmoid"])
+def test_weights_far_below_the_largest(scoring, top, T):
+    """Picks down to e^-56 of the largest, whose own scores may leave fp32's
+    range: each weight to fp32's precision.  The logits are exact in fp32; expf
+    (2 ulp), the sums, two divisions and a rounding near 2^-126 (2e-7) stay
+    below 2e-6, and l - top is exact."""
+    E, k = 32, 8
+    x = torch.zeros(T, 64)
+    x[:, 0], x[:, 1] = 1, 0.25 * (1 + torch.arange(T) % 4)
+    w = torch.zeros(E, 64)
+    w[:, 0], w[:, 1] = top, -8.0 * torch.arange(E)
+    w[k + 3:, 0] -= 200
+    idx, wt = moeq.moe_route_scored(x.bfloat16().cuda(), w.cuda(), k, scoring=scoring)
+    ref, rw, _ = M.route_scored(x.double().numpy(), w.double().numpy(), k, scoring=scoring)
+    np.testing.assert_array_equal(idx.cpu().numpy(), ref)
+    np.testing.assert_allclose(wt.cpu().numpy(), rw, rtol=1e-5, atol=0)
+
+
 def check_picks(x, w, k, bias=None, rtol=1e-5, **kw):
     idx, wt = moeq.moe_route_scored(x.cuda(), w.cuda(), k, bias=None if bias is None else bias.cuda(), **kw)
     ref, rw, _ = M.route_scored(x.double().numpy(), w.double().numpy(), k,
