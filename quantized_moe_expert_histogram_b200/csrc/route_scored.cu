@@ -12,7 +12,10 @@
 // product is exact: the experts that could change which groups stay, then
 // the experts whose order among the picks, or whose place in or out of
 // them, is open.  A token's rows that hold no finite bound (overflow, NaN,
-// Inf) are evaluated in fp64 throughout.
+// Inf) are evaluated in fp64 throughout, and where scores are compared (not the
+// logits) so are those with a bound above 0.05: |x| |W_e| above 3300 at d =
+// 4096.  A batch of such tokens is slow: 250 of them, 256 experts, sigmoid with a
+// bias, 1093 us in place of 39 (softmax with a bias, which lists them, 95).
 //
 // Where the scores do not need each other an open expert costs one fp64 dot
 // product: sigmoid; without a bias and without sums of two, where c rises with
